@@ -295,6 +295,172 @@ zipccl_status zipccl_codebook_phase(int phase, int *base_offset, uint8_t *lens16
  */
 zipccl_status zipccl_codebook_rebuild_phase(int phase, int *base_offset, uint8_t *lens16);
 
+/*
+ * ---------------------------------------------------------------- operators around the exchange
+ *
+ * What makes and what uses the exchanged tensors in training of
+ * mixture-of-experts models: routing (which token goes to which expert), the
+ * plan of the experts' chunks, dispatch and combine (to and from the rows
+ * that zipccl_compress packs, one chunk per expert), and the optimizer step
+ * between zipccl_decompress_reduce (gradient shard) and zipccl_compress
+ * (parameters).  The conventions above hold, with these differences:
+ *   - pointers need only the alignment of their element type; 16-byte
+ *     aligned rows and tensors are the fast path;
+ *   - the calls record no device status: every index read from device memory
+ *     is checked against its range, and what is out of range takes no part,
+ *     as each call says;
+ *   - only zipccl_moe_plan needs a workspace.
+ * Sums, softmax statistics, weights and states are computed in 32 bits; a
+ * result of a 16-bit type is rounded once, to nearest even.  No call's
+ * result depends on timing: no atomics on results, sums in a fixed order.
+ */
+typedef enum {
+    ZIPCCL_TYPE_F32 = 0,
+    ZIPCCL_TYPE_BF16 = 1,
+    ZIPCCL_TYPE_F16 = 2
+} zipccl_type;
+
+typedef enum { ZIPCCL_SCORE_SOFTMAX = 0, ZIPCCL_SCORE_SIGMOID = 1 } zipccl_score;
+typedef enum { ZIPCCL_GROUP_MAX = 0, ZIPCCL_GROUP_TOP2 = 1 } zipccl_group_score;
+
+typedef struct {
+    uint32_t top_k;       /* experts of a token: 1 .. min(32, groups_kept * experts / groups) */
+    int32_t score;        /* zipccl_score */
+    int32_t renormalize;  /* divide the chosen scores by their sum */
+    float scale;          /* factor on the weights */
+    uint32_t groups;      /* 1 .. 32, a divisor of the expert count; consecutive experts form a group */
+    uint32_t groups_kept; /* groups a token may choose from: 1 .. groups */
+    int32_t group_score;  /* zipccl_group_score: a group's largest choice score, or the sum of its two largest */
+} zipccl_route_options;
+
+/*
+ * Experts and weights of every token.  With l the logits of a token (a
+ * +infinite one counts as the largest finite float):
+ *   score    s_e = exp(l_e) / sum exp(l)   or   1 / (1 + exp(-l_e))
+ *   choice   c_e = s_e + bias_e (d_bias: experts floats, or NULL: 0)
+ *   groups   the groups_kept best by their group score (equal: lower group)
+ *   experts  the top_k largest c_e in the kept groups, in descending order
+ *            (equal: lower expert)
+ *   weight   scale * s_e, or scale * s_e / sum of the chosen s
+ * The bias takes part in the choice only.  An expert whose logit is -infinite
+ * or NaN, or whose c_e is, is not eligible and takes no part in the softmax
+ * (the latter: in the choice); d_mask (tokens bytes, or NULL) excludes the
+ * tokens whose byte is 0.  Where fewer than top_k experts are eligible the
+ * remaining ids are -1 with weight 0; chosen scores that sum to 0 give
+ * weights 0.
+ *   d_logits: [tokens][experts] of `type`, rows row_stride >= experts values
+ *     apart, 1 <= experts <= 1024;  d_weights: [tokens][top_k] float;
+ *     d_ids: [tokens][top_k] int32.  tokens * top_k < 2^31.
+ */
+zipccl_status zipccl_moe_route(const void *d_logits, int type, uint64_t row_stride, uint64_t tokens,
+                               uint32_t experts, const zipccl_route_options *options,
+                               const float *d_bias, const uint8_t *d_mask, float *d_weights,
+                               int32_t *d_ids, void *stream);
+
+/*
+ * Gradient of zipccl_moe_route by the logits, for the same logits, options
+ * and the ids it chose (distinct for a token; ids outside the experts take no
+ * part): d_grad_logits [tokens][experts] of `type`, contiguous, fully
+ * written.  The choice itself has no gradient, nor has the bias.
+ */
+zipccl_status zipccl_moe_route_backward(const float *d_grad_weights, const void *d_logits, int type,
+                                        uint64_t row_stride, uint64_t tokens, uint32_t experts,
+                                        const zipccl_route_options *options, const int32_t *d_ids,
+                                        void *d_grad_logits, void *stream);
+
+/*
+ * Chunk layout of `pairs` = tokens * top_k token-expert pairs with experts
+ * d_ids: chunk e holds the pairs of expert e in the order of d_ids.
+ *   d_counts [experts]: rows of each chunk;
+ *   d_offsets [experts + 1]: first row of each chunk, and the rows in all;
+ *   d_slots [pairs]: row of each pair.  A pair whose id is outside
+ *     0 .. experts-1 is dropped: its slot is -1 - row, with a row of its own
+ *     after the last chunk's, so that pairs and rows stay one to one.
+ * pairs < 2^31, experts <= 1024.  d_ws: 256-byte aligned, at least
+ * zipccl_moe_plan_workspace_bytes bytes (0 for few pairs: NULL is allowed).
+ */
+zipccl_status zipccl_moe_plan_workspace_bytes(uint64_t pairs, uint32_t experts, uint64_t *out_bytes);
+zipccl_status zipccl_moe_plan(const int32_t *d_ids, uint64_t pairs, uint32_t experts,
+                              int32_t *d_counts, int32_t *d_offsets, int32_t *d_slots, void *d_ws,
+                              uint64_t ws_bytes, void *stream);
+
+/*
+ * Rows of the experts' chunks: d_rows[slot] = d_x[token] for each pair; the
+ * rows of dropped pairs are zeros.  d_x: [tokens][hidden] of `type`, rows
+ * row_stride values apart (0: the same row for all); d_slots:
+ * [tokens][top_k], top_k <= 32; d_rows: [tokens * top_k][hidden].  A slot
+ * outside the rows is skipped.  d_x and d_rows must not overlap.
+ * The backward call sums: d_grad_x[token] = sum over the token's pairs of
+ * d_grad_rows[slot], dropped pairs left out.
+ */
+zipccl_status zipccl_moe_dispatch(const void *d_x, int type, uint64_t row_stride, uint64_t tokens,
+                                  uint32_t top_k, uint64_t hidden, const int32_t *d_slots,
+                                  void *d_rows, void *stream);
+zipccl_status zipccl_moe_dispatch_backward(const void *d_grad_rows, int type, uint64_t tokens,
+                                           uint32_t top_k, uint64_t hidden, const int32_t *d_slots,
+                                           void *d_grad_x, void *stream);
+
+/*
+ * The experts' rows back at their tokens: d_y[token] = d_residual[token] +
+ * sum over the token's pairs of weight * d_rows[slot].  Dropped pairs (and
+ * slots outside the rows) take no part, whatever their rows hold; a token
+ * without pairs gets its residual, or 0.  d_weights: [tokens][top_k] or NULL
+ * (1); d_residual: [tokens][hidden] or NULL (0), may be d_y.
+ * The backward call: d_grad_rows[slot] = weight * d_grad_y[token] (0 for
+ * dropped pairs) and, unless NULL, d_grad_weights = <d_grad_y[token],
+ * d_rows[slot]> (0 for dropped pairs).
+ */
+zipccl_status zipccl_moe_combine(const void *d_rows, int type, uint64_t tokens, uint32_t top_k,
+                                 uint64_t hidden, const int32_t *d_slots, const float *d_weights,
+                                 const void *d_residual, void *d_y, void *stream);
+zipccl_status zipccl_moe_combine_backward(const void *d_grad_y, const void *d_rows, int type,
+                                          uint64_t tokens, uint32_t top_k, uint64_t hidden,
+                                          const int32_t *d_slots, const float *d_weights,
+                                          void *d_grad_rows, float *d_grad_weights, void *stream);
+
+/*
+ * One AdamW step, in place, over n_tensors tensors (host array) in as few
+ * launches as their records fit.  With g the gradient (times *d_grad_scale,
+ * a device float, unless NULL):
+ *   m = beta1 m + (1 - beta1) g          v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) *
+ *       m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * and, where d_copy is set, d_copy = bf16(p).
+ * param_type: F32 or BF16 (then p is rounded at every step);  grad_type: F32
+ * or BF16.
+ * state_bits 32: d_exp_avg and d_exp_avg_sq hold m and v as floats.
+ * state_bits 8: they hold m and sqrt(v) as E4M3 bytes (4 exponent, 3 mantissa
+ * bits) times one float scale for each block of ZIPCCL_ADAMW_BLOCK
+ * consecutive values of a tensor, in d_avg_scale and d_sq_scale
+ * (ceil(n / ZIPCCL_ADAMW_BLOCK) each).  The new scale is the block's largest
+ * finite magnitude over 448 (at least 2^-126); a positive sqrt(v) is never
+ * stored as 0, so that no step is divided by eps alone; what is not finite is
+ * stored as NaN, in its own place only.  The step itself uses the new m and v
+ * before they are rounded.  Zero bytes and any finite scale are a valid start.
+ * 0 <= beta1, beta2 < 1; lr, eps, weight_decay >= 0; step >= 1.  The options
+ * are launch parameters: a captured graph replays them unchanged.
+ */
+#define ZIPCCL_ADAMW_BLOCK 256u
+typedef struct {
+    void *d_param;
+    const void *d_grad;
+    void *d_exp_avg;
+    void *d_exp_avg_sq;
+    void *d_copy;       /* nullable: BF16 copy of the new parameters */
+    float *d_avg_scale; /* state_bits 8 only */
+    float *d_sq_scale;  /* state_bits 8 only */
+    uint64_t n;
+} zipccl_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    uint64_t step; /* 1 for the first */
+} zipccl_adamw_options;
+
+zipccl_status zipccl_adamw_step(const zipccl_adamw_tensor *tensors, uint32_t n_tensors, int param_type,
+                                int grad_type, int state_bits, const zipccl_adamw_options *options,
+                                const float *d_grad_scale, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,7 +13,8 @@ kernels; there is no CPU path.  PyTorch provides device memory and streams.
 
 Low-level names mirror the C ABI (``zipccl_compress`` ...) and take raw
 pointers; ``compress`` / ``decompress`` / ``decompress_reduce`` are the same
-calls on torch tensors.
+calls on torch tensors.  ``operators`` adds what makes and uses the exchanged
+tensors: routing to experts, dispatch and combine, the AdamW step.
 """
 from __future__ import annotations
 
@@ -44,6 +45,9 @@ EXPORTED_SYMBOLS = [
     "zipccl_decompress_reduce_noalloc",
     "zipccl_predict_chunk_bytes",
     "zipccl_choose_compressed", "zipccl_selftest_bounded_wait", "zipccl_profile_encode_events",
+    "zipccl_moe_route", "zipccl_moe_route_backward", "zipccl_moe_plan_workspace_bytes", "zipccl_moe_plan",
+    "zipccl_moe_dispatch", "zipccl_moe_dispatch_backward", "zipccl_moe_combine", "zipccl_moe_combine_backward",
+    "zipccl_adamw_step",
 ]
 
 _lock = threading.Lock()
@@ -121,6 +125,8 @@ def load(build_if_missing: bool = True):
         L.zipccl_choose_compressed.restype = ctypes.c_int
         L.zipccl_choose_compressed.argtypes = [u64, ctypes.c_float, dbl, dbl, dbl, dbl, ctypes.POINTER(ctypes.c_int),
                                                ctypes.POINTER(dbl)]
+        from . import operators_abi
+        operators_abi.declare(L)
         _lib = L
         return L
 
@@ -392,3 +398,21 @@ def decompress_reduce(peer_chunks, n: int, out=None, ws=None, stream=None):
                                   out.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr(stream))
     _check(st, "zipccl_decompress_reduce")
     return out
+
+
+from .operators_abi import *  # noqa: E402,F401,F403
+from .operators_abi import __all__ as _abi_names  # noqa: E402
+
+_tensor_names = ["MoePlan", "moe_route", "moe_route_backward", "moe_plan", "moe_dispatch", "moe_dispatch_backward",
+                 "moe_combine", "moe_combine_backward", "adamw_step", "adamw_state", "ADAMW_BLOCK"]
+__all__ += [*_abi_names, *_tensor_names]
+
+
+def __getattr__(name):
+    """The operators on tensors need torch, which this module imports only when it is used."""
+    if name not in _tensor_names:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import operators
+    for n in _tensor_names:
+        globals()[n] = getattr(operators, n)
+    return globals()[name]

@@ -1,0 +1,42 @@
+// zc_ops.cuh -- shared by the operators around the exchange (routing, plan,
+// dispatch, combine, optimizer step): value types, 16-byte vectors of them,
+// streaming loads and stores.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "zipccl.h"
+
+namespace zc {
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+
+template <class T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+
+// kN values moved as one 16-byte access, or a single value where rows or
+// pointers are not 16-byte aligned.
+template <class T, int kN>
+struct alignas(sizeof(T) * kN) Pack {
+  T v[kN];
+};
+
+inline bool host_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+inline uint32_t type_bytes(int type) {
+  return type == ZIPCCL_TYPE_F32 ? 4u : (type == ZIPCCL_TYPE_BF16 || type == ZIPCCL_TYPE_F16) ? 2u : 0u;
+}
+
+}  // namespace zc
