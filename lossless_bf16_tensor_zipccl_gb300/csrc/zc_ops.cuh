@@ -33,6 +33,37 @@ struct alignas(sizeof(T) * kN) Pack {
   T v[kN];
 };
 
+// kN values rounded to T, in pairs where T has 16 bits.
+template <class T, int kN>
+__device__ __forceinline__ Pack<T, kN> rounded(const float (&x)[kN]) {
+  Pack<T, kN> p;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) p.v[i] = from_float<T>(x[i]);
+  return p;
+}
+template <>
+__device__ __forceinline__ Pack<__nv_bfloat16, 8> rounded<__nv_bfloat16, 8>(const float (&x)[8]) {
+  Pack<__nv_bfloat16, 8> p;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const __nv_bfloat162 y = __floats2bfloat162_rn(x[i], x[i + 1]);
+    p.v[i] = y.x;
+    p.v[i + 1] = y.y;
+  }
+  return p;
+}
+template <>
+__device__ __forceinline__ Pack<__half, 8> rounded<__half, 8>(const float (&x)[8]) {
+  Pack<__half, 8> p;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const __half2 y = __floats2half2_rn(x[i], x[i + 1]);
+    p.v[i] = y.x;
+    p.v[i + 1] = y.y;
+  }
+  return p;
+}
+
 inline bool host_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 inline uint32_t type_bytes(int type) {
