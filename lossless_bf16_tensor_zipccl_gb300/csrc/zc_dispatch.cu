@@ -15,7 +15,6 @@ constexpr uint32_t kMaxTopK = 32;
 constexpr int kRowThreads = 256;
 constexpr int kMaxDevices = 64;
 constexpr uint32_t kPipeSmemMax = 110 << 10;
-constexpr uint64_t kPipeTokens = 1, kPipeBytes = 1;
 
 struct RowArgs {
   const void* src;        // dispatch: x;  combine: rows;  combine backward: rows
@@ -30,16 +29,20 @@ struct RowArgs {
   uint64_t rows;          // tokens * top_k
 };
 
-// Two forms of each kernel.
-//  - Plain: blockDim.x threads share a token and take one vector of its row at
-//    a time; blockDim.y tokens share a block, so that narrow rows fill it too.
-//    A vector is 16 bytes, or one value where a buffer is not 16-byte aligned.
-//    It has the shortest chain from launch to result: for few tokens.
-//  - Piped: the rows are gathered, so a warp that loads, sums and stores waits
-//    for a slot and then for a row each time, and registers hold few loads
-//    (16,384 x 4,096 bf16, two pairs: combine 73 us, backward 124).  Here each
-//    warp keeps a ring of row pieces in shared memory filled by asynchronous
-//    copies, 8 KB ahead of what it sums, over all its tokens in turn.
+// Two forms of the kernels.
+//  - Plain: blockDim.x threads share a token, blockDim.y tokens a block, so
+//    that narrow rows fill it too.  Dispatch of rows that are multiples of 16
+//    bytes takes it, a vector at a time: it only stores what it has loaded
+//    once, and stores wait for nothing (16,384 x 4,096 bf16, two pairs: 61 us,
+//    99% of the measured copy rate).  Elsewhere it goes value by value, for
+//    buffers that do not start at a multiple of 16 bytes.
+//  - Piped: combine and its gradient gather rows, so a warp that loads, sums
+//    and stores waits for a slot and then for a row each time, and more loads
+//    in registers cost warps (the same size: 73 and 124 us at best).  Here
+//    each warp keeps a ring of row pieces in shared memory, filled by
+//    asynchronous copies two stages ahead of what it sums, over all its rows
+//    in turn: 61 and 102 us, 99% of the copy rate.  For a few tokens it is
+//    0.3 us slower than the plain form by vectors, which is not kept for that.
 // Rows whose size is no multiple of 16 bytes start at any place within 16.
 // The piped form (and dispatch) then works on the vectors of the row that is
 // written, and takes the other rows' bytes from the aligned pieces that cover
@@ -67,69 +70,48 @@ __global__ void __launch_bounds__(kRowThreads) zc_dispatch_kernel(RowArgs a, uin
 
 // y[token] = residual + sum over its pairs of weight * rows[slot], in pair
 // order, held in 32 bits and rounded once.
-template <class T, int N>
+template <class T>
 __global__ void __launch_bounds__(kRowThreads) zc_combine_kernel(RowArgs a) {
-  using P = Pack<T, N>;
-  const uint64_t t = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y, nv = a.hidden / N;
+  const uint64_t t = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= a.tokens) return;
   const int32_t* slots = a.slots + t * a.top_k;
-  const P* src = static_cast<const P*>(a.src);
-  for (uint64_t v = threadIdx.x; v < nv; v += blockDim.x) {
-    float y[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) y[i] = 0.0f;
+  const T* src = static_cast<const T*>(a.src);
+  for (uint64_t i = threadIdx.x; i < a.hidden; i += blockDim.x) {
+    float y = 0.0f;
     for (uint32_t k = 0; k < a.top_k; ++k) {
       const int32_t s = slots[k];
       if (s < 0 || (uint64_t)s >= a.rows) continue;
       const float w = a.weights ? a.weights[t * a.top_k + k] : 1.0f;
-      const P p = src[(uint64_t)s * nv + v];
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = fmaf(w, to_float(p.v[i]), y[i]);
+      y = fmaf(w, to_float(src[(uint64_t)s * a.hidden + i]), y);
     }
-    if (a.side) {
-      const P p = static_cast<const P*>(a.side)[t * nv + v];
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] += to_float(p.v[i]);
-    }
-    static_cast<P*>(a.dst)[t * nv + v] = rounded<T, N>(y);
+    if (a.side) y += to_float(static_cast<const T*>(a.side)[t * a.hidden + i]);
+    static_cast<T*>(a.dst)[t * a.hidden + i] = from_float<T>(y);
   }
 }
 
 // grad_rows[slot] = weight * grad[token], grad_weight = <grad[token], rows[slot]>.
-// The products are summed along a fixed tree: a thread's vectors, lanes, warps.
-template <class T, int N>
+// The products are summed along a fixed tree: a thread's, lanes, warps.
+template <class T>
 __global__ void __launch_bounds__(kRowThreads) zc_combine_backward_kernel(RowArgs a) {
-  using P = Pack<T, N>;
   __shared__ float s_dot[kRowThreads / 32];
-  const uint64_t t = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y, nv = a.hidden / N;
+  const uint64_t t = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = t < a.tokens;
   const uint32_t width = min(blockDim.x, 32u);
   const uint32_t warp = (threadIdx.y * blockDim.x + threadIdx.x) / 32, warps = blockDim.x / 32;
-  const P* g = static_cast<const P*>(a.side) + t * nv;
-  P zero;
-#pragma unroll
-  for (int i = 0; i < N; ++i) zero.v[i] = from_float<T>(0.0f);
+  const T* g = static_cast<const T*>(a.side) + t * a.hidden;
   for (uint32_t k = 0; k < a.top_k; ++k) {
     const int32_t s = live ? a.slots[t * a.top_k + k] : INT32_MIN;
     const uint64_t row = (uint64_t)(s < 0 ? ~s : s);
     const bool in = row < a.rows;
     const float w = !in || s < 0 ? 0.0f : a.weights ? a.weights[t * a.top_k + k] : 1.0f;
-    const P* r = static_cast<const P*>(a.src) + row * nv;
-    P* out = static_cast<P*>(a.dst) + row * nv;
+    const T* r = static_cast<const T*>(a.src) + row * a.hidden;
+    T* out = static_cast<T*>(a.dst) + row * a.hidden;
     float dot = 0.0f;
     if (in)
-      for (uint64_t v = threadIdx.x; v < nv; v += blockDim.x) {
-        P o = zero;
-        if (s >= 0) {
-          const P p = g[v], q = r[v];
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float x = to_float(p.v[i]);
-            dot = fmaf(x, to_float(q.v[i]), dot);
-            o.v[i] = from_float<T>(w * x);
-          }
-        }
-        out[v] = o;
+      for (uint64_t i = threadIdx.x; i < a.hidden; i += blockDim.x) {
+        const float x = s < 0 ? 0.0f : to_float(g[i]);
+        if (s >= 0) dot = fmaf(x, to_float(r[i]), dot);
+        out[i] = from_float<T>(s < 0 ? 0.0f : w * x);
       }
     if (!a.grad_weights) continue;
     for (uint32_t o = width / 2; o; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
@@ -648,16 +630,17 @@ dim3 row_block(uint64_t nv) {
   return dim3(x, kRowThreads / x);
 }
 
-template <class T, int N>
+// Plain form, kN values at a time for dispatch and one otherwise.
+template <class T, int kN>
 cudaError_t plain_launch(RowOp op, const RowArgs& a, cudaStream_t s) {
-  const dim3 block = row_block(a.hidden / N);
+  const dim3 block = row_block(a.hidden / kN);
   const uint32_t grid = (a.tokens + block.y - 1) / block.y;
   if (op == RowOp::kDispatch)
-    zc_dispatch_kernel<Pack<T, N>><<<grid, block, 0, s>>>(a, a.stride / N, a.hidden / N);
+    zc_dispatch_kernel<Pack<T, kN>><<<grid, block, 0, s>>>(a, a.stride / kN, a.hidden / kN);
   else if (op == RowOp::kCombine)
-    zc_combine_kernel<T, N><<<grid, block, 0, s>>>(a);
+    zc_combine_kernel<T><<<grid, block, 0, s>>>(a);
   else
-    zc_combine_backward_kernel<T, N><<<grid, block, 0, s>>>(a);
+    zc_combine_backward_kernel<T><<<grid, block, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -703,7 +686,8 @@ cudaError_t pipe_form(RowOp op, const RowArgs& a, uint32_t log_lanes, uint64_t v
     return pipe_launch<zc_combine_backward_pipe_kernel<T, V, kOdd>>(
         a, q, q.pieces > 1 ? (uint64_t)a.tokens * groups : a.tokens, groups * (stage * (kStageVec / V * kStages) + (kOdd ? stage + 32 : 0)), s);
   }
-  return pipe_launch<zc_dispatch_odd_kernel<T, V>>(a, q, items, groups * (lanes * V + 4) * 16 * 2, s);
+  if constexpr (kOdd) return pipe_launch<zc_dispatch_odd_kernel<T, V>>(a, q, items, groups * (lanes * V + 4) * 16 * 2, s);
+  return cudaErrorInvalidValue;
 }
 
 template <class T, bool kOdd>
@@ -720,15 +704,14 @@ cudaError_t pipe_by_width(RowOp op, const RowArgs& a, cudaStream_t s) {
 template <class T>
 cudaError_t row_form(RowOp op, const RowArgs& a, cudaStream_t s) {
   constexpr uint32_t z = sizeof(T), N = 16 / z;
-  const bool base = host_aligned(a.src, 16) && host_aligned(a.side, 16) && host_aligned(a.dst, 16);
-  const bool even = base && a.hidden % N == 0 && (op != RowOp::kDispatch || a.stride % N == 0);
-  const uint64_t bytes = (uint64_t)a.tokens * a.top_k * a.hidden * z;
-  const bool many = a.hidden * z < (1ull << 30) && a.tokens >= kPipeTokens && bytes >= kPipeBytes &&
-                    (uint64_t)a.tokens * ((a.hidden + 511) / 512 + 1) < (1ull << 31);
-  if (even && (op == RowOp::kDispatch || !many)) return plain_launch<T, N>(op, a, s);
-  if (even) return pipe_by_width<T, false>(op, a, s);
-  if (base && many) return pipe_by_width<T, true>(op, a, s);
-  return plain_launch<T, 1>(op, a, s);
+  // the piped form starts at multiples of 16 bytes and counts pieces in 32 bits
+  const bool base = host_aligned(a.src, 16) && host_aligned(a.side, 16) && host_aligned(a.dst, 16) && a.hidden &&
+                    a.hidden * z < (1ull << 30) && (uint64_t)a.tokens * ((a.hidden + 511) / 512 + 1) < (1ull << 31);
+  const bool even = a.hidden % N == 0 && (op != RowOp::kDispatch || a.stride % N == 0);
+  if (!base) return plain_launch<T, 1>(op, a, s);
+  if (!even) return pipe_by_width<T, true>(op, a, s);
+  if (op == RowOp::kDispatch) return plain_launch<T, N>(op, a, s);
+  return pipe_by_width<T, false>(op, a, s);
 }
 
 zipccl_status rows(RowOp op, RowArgs& a, int type, uint64_t tokens, uint32_t top_k, uint64_t hidden, void* stream) {

@@ -15,7 +15,7 @@ namespace {
 constexpr uint32_t kMaxExperts = 1024;
 constexpr uint32_t kMaxTopK = 32;
 constexpr uint32_t kMaxGroups = 32;
-constexpr int kRouteThreads = 128;
+constexpr int kRouteThreads = 256;
 
 struct RouteArgs {
   const void* logits;
@@ -28,7 +28,8 @@ struct RouteArgs {
   uint64_t stride;       // values between rows
   uint32_t tokens, experts, top_k, groups, kept, group_size;
   float scale;
-  bool softmax, renormalize, top2;
+  uint32_t group_lanes;  // lanes of a group where groups are whole lanes, a power of two of them; else 0
+  bool softmax, renormalize, top2, wide, wide_out;
 };
 
 // Order-preserving bits of a choice score; 0 stands for "cannot be chosen"
@@ -39,164 +40,200 @@ __device__ __forceinline__ uint32_t order_bits(float c) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-template <int L>
-__device__ __forceinline__ float seg_max(float v) {
-#pragma unroll
-  for (int o = L / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
+__device__ __forceinline__ float from_order_bits(uint32_t u) {
+  return u == 0 ? -INFINITY : __uint_as_float((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
 }
-template <int L>
-__device__ __forceinline__ float seg_sum(float v) {
+__device__ __forceinline__ float warp_max(float v) { return from_order_bits(__reduce_max_sync(kAll, order_bits(v))); }
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
-}
-template <int L>
-__device__ __forceinline__ uint32_t seg_max_bits(uint32_t v) {
-  if (L == 32) return __reduce_max_sync(kAll, v);
-#pragma unroll
-  for (int o = L / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
 
-// L lanes hold a token, V consecutive experts each.
-template <class T, int L, int V>
-__global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
-  constexpr int kTok = kRouteThreads / L;
-  __shared__ float s_val[kTok][L * V + 1];  // choice scores, for the groups
-  __shared__ float s_group[kTok][kMaxGroups];
-  __shared__ float s_pick[kTok][kMaxTopK];
-  __shared__ int32_t s_id[kTok][kMaxTopK];
-  const int lane = threadIdx.x % L, t = threadIdx.x / L;
-  const uint64_t tok = (uint64_t)blockIdx.x * kTok + t;
-  const bool live = tok < a.tokens && (!a.mask || a.mask[tok]);
-  const T* row = static_cast<const T*>(a.logits) + (tok < a.tokens ? tok : 0) * a.stride;
-  const uint32_t e0 = lane * V;
+// The hardware's reciprocal (1 ulp): a score is off by 2 ulp with it, and it
+// takes one instruction where a division takes 10.
+__device__ __forceinline__ float quick_rcp(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sigmoid(float l) { return quick_rcp(1.0f + expf(-l)); }
 
-  float l[V];
-  uint32_t fit = 0;
-  float top = -INFINITY;
+// V values of a row from place e0 on; -inf where the row has ended.  `wide`:
+// every row starts and ends at a multiple of 16 bytes.
+template <class T, int V>
+__device__ __forceinline__ void load_logits(const T* row, uint32_t e0, uint32_t experts, bool wide, float (&l)[V]) {
+  constexpr int N = 16 / sizeof(T) < V ? 16 / sizeof(T) : V;
+#pragma unroll
+  for (int j = 0; j < V; j += N) {
+    if (wide) {
+      Pack<T, N> p;
+      const bool in = e0 + j < experts;
+      if (in) p = *reinterpret_cast<const Pack<T, N>*>(row + e0 + j);
+#pragma unroll
+      for (int i = 0; i < N; ++i) l[j + i] = in ? to_float(p.v[i]) : -INFINITY;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) l[j + i] = e0 + j + i < experts ? to_float(row[e0 + j + i]) : -INFINITY;
+    }
+  }
+}
+
+// Scores of V logits: the softmax over the whole row, or sigmoids.  A logit
+// that is -inf or NaN becomes -inf and takes no part, +inf the largest float.
+template <int V>
+__device__ __forceinline__ void settle(float (&l)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) l[j] = l[j] > -INFINITY ? fminf(l[j], FLT_MAX) : -INFINITY;
+}
+template <int V>
+__device__ __forceinline__ void softmax(const float (&l)[V], float (&s)[V], float* top, float* sum) {
+  float m = l[0], z = 0.0f;
+#pragma unroll
+  for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
+  m = warp_max(m);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const float x = live && e0 + j < a.experts ? to_float(row[e0 + j]) : -INFINITY;
-    if (x > -INFINITY) fit |= 1u << j;
-    l[j] = x > -INFINITY ? fminf(x, FLT_MAX) : -INFINITY;
-    top = fmaxf(top, l[j]);
+    s[j] = l[j] > -INFINITY ? expf(l[j] - m) : 0.0f;
+    z += s[j];
   }
-  const bool by_logit = a.softmax && !a.bias && (a.groups == 1 || !a.top2);
-  float s[V];
-  if (a.softmax) {
-    if (!by_logit || !a.renormalize) {
-      top = seg_max<L>(top);
-      float sum = 0.0f;
+  z = warp_sum(z);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        s[j] = (fit >> j & 1) ? expf(l[j] - top) : 0.0f;
-        sum += s[j];
-      }
-      sum = seg_sum<L>(sum);
+  for (int j = 0; j < V; ++j) s[j] = z > 0.0f ? s[j] / z : 0.0f;
+  *top = m;
+  *sum = z;
+}
+
+// Group scores of a token whose choice scores the lanes hold: groups of
+// 1 << log_lanes whole lanes, or of any size through shared memory.  Returns
+// the kept groups, a bit each.
+template <int V>
+__device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, const float (&c)[V], float* shared, uint32_t lane) {
+  float hi = -INFINITY, lo = -INFINITY;
+  uint32_t stride = 1;  // lanes from a group's score to the next's
+  if (a.group_lanes) {
+    stride = a.group_lanes;
 #pragma unroll
-      for (int j = 0; j < V; ++j) s[j] = s[j] / sum;
+    for (int j = 0; j < V; ++j) {
+      lo = fmaxf(lo, fminf(hi, c[j]));
+      hi = fmaxf(hi, c[j]);
+    }
+    for (uint32_t o = 1; o < stride; o <<= 1) {
+      const float h = __shfl_xor_sync(kAll, hi, o), l = __shfl_xor_sync(kAll, lo, o);
+      lo = fmaxf(fminf(hi, h), fmaxf(lo, l));
+      hi = fmaxf(hi, h);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) s[j] = 1.0f / (1.0f + expf(-l[j]));
-  }
-  float c[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    c[j] = by_logit ? l[j] : s[j];
-    if (a.bias && e0 + j < a.experts) c[j] += a.bias[e0 + j];
-    if (!(fit >> j & 1) || !(c[j] > -INFINITY)) c[j] = -INFINITY;
-  }
-  if (a.groups > 1) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) s_val[t][e0 + j] = c[j];
+    for (int j = 0; j < V; ++j) shared[lane * V + j] = c[j];
     __syncwarp();
-    for (uint32_t g = lane; g < a.groups; g += L) {
-      float hi = -INFINITY, lo = -INFINITY;
+    if (lane < a.groups)
       for (uint32_t i = 0; i < a.group_size; ++i) {
-        const float x = s_val[t][g * a.group_size + i];
+        const float x = shared[lane * a.group_size + i];
         lo = fmaxf(lo, fminf(hi, x));
         hi = fmaxf(hi, x);
       }
-      s_group[t][g] = (a.top2 && lo > -INFINITY ? hi + lo : hi) + 0.0f;
-    }
     __syncwarp();
-    // a group is kept if fewer than `kept` groups come before it
-    uint32_t keep = 0;
-    for (uint32_t g = lane; g < a.groups; g += L) {
-      uint32_t before = 0;
-      const float x = s_group[t][g];
-      for (uint32_t h = 0; h < a.groups; ++h) {
-        const float y = s_group[t][h];
-        before += y > x || (y == x && h < g);
-      }
-      if (before < a.kept) keep |= 1u << g;
-    }
+  }
+  // a group is kept if fewer than `kept` groups come before it; equal: the lower first
+  const float mine = (a.top2 && lo > -INFINITY ? hi + lo : hi) + 0.0f;
+  const uint32_t g = lane / stride;
+  uint32_t before = 0;
+  for (uint32_t h = 0; h < a.groups; ++h) {
+    const float y = __shfl_sync(kAll, mine, h * stride);
+    before += y > mine || (y == mine && h < g);
+  }
+  const uint32_t lanes = __ballot_sync(kAll, g < a.groups && before < a.kept);
+  if (stride == 1) return lanes;
+  uint32_t keep = 0;
+  for (uint32_t h = 0; h < a.groups; ++h) keep |= (lanes >> (h * stride) & 1) << h;
+  return keep;
+}
+
+// A warp takes a token, a lane V consecutive experts.  The choice scores lie
+// in shared memory as ordered bits; each lane knows the best of its own, and
+// top_k times the warp finds the best of these, its place among the lane's V
+// (the lowest place of the lowest lane is the lowest expert among equals), and
+// what is then best in that lane: no step takes one lane's branch.
+template <class T, int V>
+__global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
+  __shared__ __align__(16) uint32_t s_key[kRouteThreads / 32][32 * V];
+  const uint32_t lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const uint64_t tok = (uint64_t)blockIdx.x * (kRouteThreads / 32) + w;
+  if (tok >= a.tokens) return;
+  const T* row = static_cast<const T*>(a.logits) + tok * a.stride;
+  const uint32_t e0 = lane * V;
+  uint32_t* keys = s_key[w];
+  const bool live = !a.mask || a.mask[tok];
+  float top = 0.0f, sum = 1.0f;
+  int32_t id = -1;  // of pair `lane`
+  if (live) {
+    float l[V], c[V];
+    load_logits<T, V>(row, e0, a.experts, a.wide, l);
+    settle(l);
+    const bool by_logit = a.softmax && !a.bias && (a.groups == 1 || !a.top2);
+    if (a.softmax && (!by_logit || !a.renormalize)) softmax(l, c, &top, &sum);
+    if (!a.softmax) {
 #pragma unroll
-    for (int o = L / 2; o; o >>= 1) keep |= __shfl_xor_sync(kAll, keep, o);
-    uint32_t g = e0 / a.group_size, r = e0 % a.group_size;
+      for (int j = 0; j < V; ++j) c[j] = sigmoid(l[j]);
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      if (e0 + j < a.experts && !(keep >> g & 1)) c[j] = -INFINITY;
-      if (++r == a.group_size) r = 0, ++g;
+      if (by_logit) c[j] = l[j];
+      if (a.bias && e0 + j < a.experts) c[j] += a.bias[e0 + j];
+      if (!(l[j] > -INFINITY) || !(c[j] > -INFINITY)) c[j] = -INFINITY;
     }
-  }
-
-  // top_k times the best that is left: the lowest lane and, there, the lowest
-  // place among equals is the lowest expert
-  uint32_t key[V], best = 0;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    key[j] = order_bits(c[j]);
-    best = max(best, key[j]);
-  }
-  const unsigned base = (threadIdx.x & 31) / L * L;
-  for (uint32_t k = 0; k < a.top_k; ++k) {
-    const uint32_t m = seg_max_bits<L>(best);
-    const unsigned who = __ballot_sync(kAll, best == m) >> base;
-    if (m == 0) {
-      if (lane == 0) s_id[t][k] = -1, s_pick[t][k] = -INFINITY;
-    } else if (lane == __ffs(who) - 1) {
-      best = 0;
-      bool found = false;
+    if (a.groups > 1) {
+      const uint32_t keep = kept_groups<V>(a, c, reinterpret_cast<float*>(keys), lane);
+      uint32_t g = e0 / a.group_size, r = e0 - g * a.group_size;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        if (!found && key[j] == m) {
-          found = true;
-          key[j] = 0;
-          s_id[t][k] = e0 + j;
-          s_pick[t][k] = a.softmax && a.renormalize ? l[j] : s[j];
-        }
-        best = max(best, key[j]);
+        if (e0 + j < a.experts && !(keep >> g & 1)) c[j] = -INFINITY;
+        if (++r == a.group_size) r = 0, ++g;
       }
     }
+    uint32_t best = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const uint32_t key = order_bits(c[j]);
+      best = max(best, key);
+      keys[e0 + j] = key;
+    }
+    for (uint32_t k = 0; k < a.top_k; ++k) {
+      __syncwarp();
+      const uint32_t m = __reduce_max_sync(kAll, best);
+      if (m == 0) break;
+      const uint32_t from = __ffs(__ballot_sync(kAll, best == m)) - 1;
+      uint32_t x = lane < V ? keys[from * V + lane] : 0;
+      const uint32_t j = __ffs(__ballot_sync(kAll, x == m)) - 1;
+      if (lane == j) {
+        x = 0;
+        keys[from * V + j] = 0;
+      }
+      const uint32_t left = __reduce_max_sync(kAll, x);
+      if (lane == from) best = left;
+      if (lane == k) id = from * V + j;
+    }
   }
-  __syncwarp();
-  float norm = 1.0f, high = 0.0f;
+  // lane k has pair k
+  if (lane >= a.top_k) id = -1;
+  float s = 0.0f;
+  if (id >= 0) {
+    const float l = fminf(to_float(row[id]), FLT_MAX);
+    s = !a.softmax ? sigmoid(l) : l;
+  }
+  if (a.softmax) {
+    if (a.renormalize) top = warp_max(id >= 0 ? s : -INFINITY);
+    s = id >= 0 ? expf(s - top) : 0.0f;
+    if (!a.renormalize) s = sum > 0.0f ? s / sum : 0.0f;  // 0: no eligible expert
+  }
   if (a.renormalize) {
-    if (a.softmax) {
-      high = -INFINITY;
-      for (uint32_t k = lane; k < a.top_k; k += L) high = fmaxf(high, s_pick[t][k]);
-      high = seg_max<L>(high);
-    }
-    norm = 0.0f;
-    for (uint32_t k = lane; k < a.top_k; k += L)
-      if (s_id[t][k] >= 0) norm += a.softmax ? expf(s_pick[t][k] - high) : s_pick[t][k];
-    norm = seg_sum<L>(norm);
+    const float all = warp_sum(s);
+    s = all > 0.0f ? s / all : 0.0f;
   }
-  if (tok >= a.tokens) return;
-  for (uint32_t k = lane; k < a.top_k; k += L) {
-    const int32_t id = s_id[t][k];
-    float w = 0.0f;
-    if (id >= 0) {
-      w = s_pick[t][k];
-      if (a.softmax && a.renormalize) w = expf(w - high);
-      if (a.renormalize) w = norm > 0.0f ? w / norm : 0.0f;
-    }
-    a.weights[tok * a.top_k + k] = w * a.scale;
-    a.ids[tok * a.top_k + k] = id;
+  if (lane < a.top_k) {
+    a.weights[tok * a.top_k + lane] = s * a.scale;
+    a.ids[tok * a.top_k + lane] = id;
   }
 }
 
@@ -205,122 +242,93 @@ __global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
 // u_k = w_k (d_k - sum_j w_j d_j) when renormalised and u_k = s_k d_k when
 // not; then dl_e = u_e - s_e sum u (softmax; the sum is 0 when renormalised)
 // or u_e (1 - s_e) (sigmoid).  Only the softmax without renormalisation has
-// to read the whole row again.
-template <class T, int L, int V>
+// to read the whole row again.  A lane has a pair first, then V experts.
+template <class T, int V>
 __global__ void __launch_bounds__(kRouteThreads) zc_route_backward_kernel(RouteArgs a) {
-  constexpr int kTok = kRouteThreads / L;
-  __shared__ float s_row[kTok][L * V + 1];
-  const int lane = threadIdx.x % L, t = threadIdx.x / L;
-  const uint64_t tok = (uint64_t)blockIdx.x * kTok + t;
-  const bool in = tok < a.tokens;
-  const T* row = static_cast<const T*>(a.logits) + (in ? tok : 0) * a.stride;
+  __shared__ __align__(16) float s_row[kRouteThreads / 32][32 * V];
+  const uint32_t lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+  const uint64_t tok = (uint64_t)blockIdx.x * (kRouteThreads / 32) + wp;
+  if (tok >= a.tokens) return;
+  const T* row = static_cast<const T*>(a.logits) + tok * a.stride;
   const uint32_t e0 = lane * V;
-#pragma unroll
-  for (int j = 0; j < V; ++j) s_row[t][e0 + j] = 0.0f;
-
-  float l[V], top = -INFINITY, sum = 1.0f;
   const bool whole = a.softmax && !a.renormalize;
+  int32_t id = lane < a.top_k ? a.ids[tok * a.top_k + lane] : -1;
+  if ((uint32_t)id >= a.experts) id = -1;
+  float d = 0.0f, s = 0.0f;
+  if (id >= 0) {
+    d = a.grad[tok * a.top_k + lane] * a.scale;
+    s = fminf(to_float(row[id]), FLT_MAX);
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) s_row[wp][e0 + j] = 0.0f;
+  float p[V], top = 0.0f, sum = 1.0f;
   if (whole) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float x = in && e0 + j < a.experts ? to_float(row[e0 + j]) : -INFINITY;
-      l[j] = x > -INFINITY ? fminf(x, FLT_MAX) : -INFINITY;
-      top = fmaxf(top, l[j]);
-    }
-    top = seg_max<L>(top);
-    sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      l[j] = l[j] > -INFINITY ? expf(l[j] - top) : 0.0f;
-      sum += l[j];
-    }
-    sum = seg_sum<L>(sum);
+    float l[V];
+    load_logits<T, V>(row, e0, a.experts, a.wide, l);
+    settle(l);
+    softmax(l, p, &top, &sum);
   }
-  constexpr int R = kMaxTopK / L;  // pairs a lane may hold
-  int32_t id[R];
-  float w[R], d[R], own[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const uint32_t k = lane + r * L;
-    id[r] = -1;
-    w[r] = d[r] = own[r] = 0.0f;
-    if (in && k < a.top_k) {
-      id[r] = a.ids[tok * a.top_k + k];
-      if (id[r] < 0 || (uint32_t)id[r] >= a.experts) id[r] = -1;
-    }
-    if (id[r] >= 0) {
-      d[r] = a.grad[tok * a.top_k + k] * a.scale;
-      own[r] = fminf(to_float(row[id[r]]), FLT_MAX);
-    }
-  }
-  float high = -INFINITY, norm = 0.0f, mean = 0.0f;
   if (a.softmax) {
-    if (a.renormalize) {
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (id[r] >= 0) high = fmaxf(high, own[r]);
-      high = seg_max<L>(high);
-    } else {
-      high = top;
-    }
+    if (a.renormalize) top = warp_max(id >= 0 ? s : -INFINITY);
+    s = id >= 0 ? expf(s - top) : 0.0f;
+    if (whole) s = sum > 0.0f ? s / sum : 0.0f;
+  } else if (id >= 0) {
+    s = sigmoid(s);
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (id[r] >= 0) {
-      own[r] = a.softmax ? expf(own[r] - high) : 1.0f / (1.0f + expf(-own[r]));
-      if (whole) own[r] = own[r] / sum;
-      norm += own[r];
-    }
+  float u = s * d;
   if (a.renormalize) {
-    norm = seg_sum<L>(norm);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      w[r] = norm > 0.0f ? own[r] / norm : 0.0f;
-      mean += w[r] * d[r];
-    }
-    mean = seg_sum<L>(mean);
+    const float all = warp_sum(s), w = all > 0.0f ? s / all : 0.0f;
+    u = w * (d - warp_sum(w * d));
   }
+  const float total = whole ? warp_sum(u) : 0.0f;
+  if (!a.softmax) u *= 1.0f - s;
   __syncwarp();
-  float all = 0.0f;
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (id[r] >= 0) {
-      float u = a.renormalize ? w[r] * (d[r] - mean) : own[r] * d[r];
-      all += u;
-      if (!a.softmax) u *= 1.0f - own[r];
-      atomicAdd(&s_row[t][id[r]], u);  // ids of a token are distinct: one add each
-    }
-  if (whole) all = seg_sum<L>(all);
+  if (id >= 0) atomicAdd(&s_row[wp][id], u);  // a token's ids are distinct: one add each
   __syncwarp();
-  if (!in) return;
   T* out = static_cast<T*>(a.grad_logits) + tok * a.experts;
+  constexpr int N = 16 / sizeof(T) < V ? 16 / sizeof(T) : V;
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-    if (e0 + j < a.experts) {
-      float g = s_row[t][e0 + j];
-      if (whole && sum > 0.0f) g -= l[j] / sum * all;  // 0: no eligible expert
-      out[e0 + j] = from_float<T>(g);
+  for (int j = 0; j < V; j += N) {
+    float g[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      g[i] = s_row[wp][e0 + j + i];
+      if (whole) g[i] -= p[j + i] * total;
     }
+    if (a.wide_out) {
+      if (e0 + j < a.experts) *reinterpret_cast<Pack<T, N>*>(out + e0 + j) = rounded<T, N>(g);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (e0 + j + i < a.experts) out[e0 + j + i] = from_float<T>(g[i]);
+    }
+  }
 }
 
-template <class T, int L, int V>
-cudaError_t route_launch(const RouteArgs& a, bool backward, cudaStream_t s) {
-  constexpr uint32_t kTok = kRouteThreads / L;
-  const uint32_t grid = (uint32_t)(((uint64_t)a.tokens + kTok - 1) / kTok);
+template <class T, int V>
+cudaError_t route_launch(RouteArgs a, bool backward, cudaStream_t s) {
+  constexpr uint32_t kTok = kRouteThreads / 32, N = 16 / sizeof(T) < V ? 16 / sizeof(T) : V;
+  // accesses of N values: rows of a multiple of N, from an aligned start
+  a.wide = host_aligned(a.logits, N * sizeof(T)) && a.stride % N == 0 && a.experts % N == 0;
+  a.wide_out = host_aligned(a.grad_logits, N * sizeof(T)) && a.experts % N == 0;
+  const uint32_t lanes = a.group_size % V ? 0 : a.group_size / V;
+  a.group_lanes = lanes & (lanes - 1) ? 0 : lanes;
+  const uint32_t grid = (a.tokens + kTok - 1) / kTok;
   if (backward)
-    zc_route_backward_kernel<T, L, V><<<grid, kRouteThreads, 0, s>>>(a);
+    zc_route_backward_kernel<T, V><<<grid, kRouteThreads, 0, s>>>(a);
   else
-    zc_route_kernel<T, L, V><<<grid, kRouteThreads, 0, s>>>(a);
+    zc_route_kernel<T, V><<<grid, kRouteThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 template <class T>
 cudaError_t route_by_experts(const RouteArgs& a, bool backward, cudaStream_t s) {
-  if (a.experts <= 64) return route_launch<T, 8, 8>(a, backward, s);
-  if (a.experts <= 128) return route_launch<T, 16, 8>(a, backward, s);
-  if (a.experts <= 256) return route_launch<T, 32, 8>(a, backward, s);
-  if (a.experts <= 512) return route_launch<T, 32, 16>(a, backward, s);
-  return route_launch<T, 32, 32>(a, backward, s);
+  if (a.experts <= 32) return route_launch<T, 1>(a, backward, s);
+  if (a.experts <= 64) return route_launch<T, 2>(a, backward, s);
+  if (a.experts <= 128) return route_launch<T, 4>(a, backward, s);
+  if (a.experts <= 256) return route_launch<T, 8>(a, backward, s);
+  if (a.experts <= 512) return route_launch<T, 16>(a, backward, s);
+  return route_launch<T, 32>(a, backward, s);
 }
 
 zipccl_status route(RouteArgs& a, int type, const zipccl_route_options* o, uint64_t tokens, uint32_t experts,
