@@ -29,7 +29,7 @@ struct RouteArgs {
   uint32_t tokens, experts, top_k, groups, kept, group_size;
   float scale;
   uint32_t group_lanes;  // lanes of a group where groups are whole lanes, a power of two of them; else 0
-  bool softmax, renormalize, top2, wide, wide_out;
+  bool softmax, renormalize, top2, wide, wide_out, wide_bias;
 };
 
 // Order-preserving bits of a choice score; 0 stands for "cannot be chosen"
@@ -40,14 +40,35 @@ __device__ __forceinline__ uint32_t order_bits(float c) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ float from_order_bits(uint32_t u) {
-  return u == 0 ? -INFINITY : __uint_as_float((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
-}
-__device__ __forceinline__ float warp_max(float v) { return from_order_bits(__reduce_max_sync(kAll, order_bits(v))); }
-__device__ __forceinline__ float warp_sum(float v) {
+// Over the L lanes of a token, which are consecutive in a warp.
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if constexpr (L == 32) {
+    return __reduce_max_sync(kAll, v);
+  } else {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    for (int o = L / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+  }
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
   return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+// The first of the token's lanes that the condition holds for; one does.
+template <int L>
+__device__ __forceinline__ uint32_t first_lane(bool x) {
+  uint32_t who = __ballot_sync(kAll, x);
+  if constexpr (L < 32) who = who >> ((threadIdx.x & 31) / L * L) & ((1u << L) - 1);
+  return __ffs(who) - 1;
 }
 
 // The hardware's reciprocal (1 ulp): a score is off by 2 ulp with it, and it
@@ -86,33 +107,32 @@ __device__ __forceinline__ void settle(float (&l)[V]) {
 #pragma unroll
   for (int j = 0; j < V; ++j) l[j] = l[j] > -INFINITY ? fminf(l[j], FLT_MAX) : -INFINITY;
 }
-template <int V>
+template <int L, int V>
 __device__ __forceinline__ void softmax(const float (&l)[V], float (&s)[V], float* top, float* sum) {
   float m = l[0], z = 0.0f;
 #pragma unroll
   for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
-  m = warp_max(m);
+  m = lanes_max<L>(m);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     s[j] = l[j] > -INFINITY ? expf(l[j] - m) : 0.0f;
     z += s[j];
   }
-  z = warp_sum(z);
+  z = lanes_sum<L>(z);
+  const float inv = z > 0.0f ? 1.0f / z : 0.0f;  // 0: no eligible expert
 #pragma unroll
-  for (int j = 0; j < V; ++j) s[j] = z > 0.0f ? s[j] / z : 0.0f;
+  for (int j = 0; j < V; ++j) s[j] *= inv;
   *top = m;
-  *sum = z;
+  *sum = inv;
 }
 
-// Group scores of a token whose choice scores the lanes hold: groups of
-// 1 << log_lanes whole lanes, or of any size through shared memory.  Returns
-// the kept groups, a bit each.
-template <int V>
-__device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, const float (&c)[V], float* shared, uint32_t lane) {
+// Leaves the choice scores of a token's kept groups and makes the others
+// -inf.  Groups are 2^n whole lanes, or of any size through shared memory.
+template <int L, int V>
+__device__ __forceinline__ void keep_groups(const RouteArgs& a, float (&c)[V], float* shared, uint32_t lane) {
   float hi = -INFINITY, lo = -INFINITY;
-  uint32_t stride = 1;  // lanes from a group's score to the next's
+  const uint32_t stride = a.group_lanes ? a.group_lanes : 1;  // lanes from a group's score to the next's
   if (a.group_lanes) {
-    stride = a.group_lanes;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       lo = fmaxf(lo, fminf(hi, c[j]));
@@ -140,100 +160,109 @@ __device__ __forceinline__ uint32_t kept_groups(const RouteArgs& a, const float 
   const uint32_t g = lane / stride;
   uint32_t before = 0;
   for (uint32_t h = 0; h < a.groups; ++h) {
-    const float y = __shfl_sync(kAll, mine, h * stride);
+    const float y = __shfl_sync(kAll, mine, h * stride, L);
     before += y > mine || (y == mine && h < g);
   }
-  const uint32_t lanes = __ballot_sync(kAll, g < a.groups && before < a.kept);
-  if (stride == 1) return lanes;
-  uint32_t keep = 0;
-  for (uint32_t h = 0; h < a.groups; ++h) keep |= (lanes >> (h * stride) & 1) << h;
-  return keep;
+  const bool kept = g < a.groups && before < a.kept;
+  if (a.group_lanes) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (!kept) c[j] = -INFINITY;
+    return;
+  }
+  const uint32_t keep = __ballot_sync(kAll, kept) >> ((threadIdx.x & 31) / L * L);
+  uint32_t e = lane * V / a.group_size, r = lane * V - e * a.group_size;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (e < a.groups && !(keep >> e & 1)) c[j] = -INFINITY;
+    if (++r == a.group_size) r = 0, ++e;
+  }
 }
 
-// A warp takes a token, a lane V consecutive experts.  The choice scores lie
-// in shared memory as ordered bits; each lane knows the best of its own, and
-// top_k times the warp finds the best of these, its place among the lane's V
-// (the lowest place of the lowest lane is the lowest expert among equals), and
-// what is then best in that lane: no step takes one lane's branch.
-template <class T, int V>
+// L lanes take a token, V consecutive experts each.  The choice scores lie in
+// shared memory as ordered bits; each lane knows the best of its own, and
+// top_k times the lanes find the best of these, its place among the V of its
+// lane (the lowest place of the lowest lane is the lowest expert among
+// equals), and what is then best in that lane: no step is one lane's alone.
+// It is bound by its instructions: 16,384 tokens of 64 experts took 389 a token
+// with all of a warp's lanes, as against L = 8.
+template <class T, int L, int V>
 __global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
-  __shared__ __align__(16) uint32_t s_key[kRouteThreads / 32][32 * V];
-  const uint32_t lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const uint64_t tok = (uint64_t)blockIdx.x * (kRouteThreads / 32) + w;
-  if (tok >= a.tokens) return;
-  const T* row = static_cast<const T*>(a.logits) + tok * a.stride;
+  static_assert(V <= L, "a lane's experts are scanned by one lane each");
+  constexpr uint32_t kTok = kRouteThreads / L;
+  __shared__ __align__(16) uint32_t s_key[kTok][L * V];
+  const uint32_t lane = threadIdx.x % L;
+  const uint32_t tok = blockIdx.x * kTok + threadIdx.x / L;
+  const bool in = tok < a.tokens;
+  const T* row = static_cast<const T*>(a.logits) + (in ? tok : 0) * a.stride;
   const uint32_t e0 = lane * V;
-  uint32_t* keys = s_key[w];
-  const bool live = !a.mask || a.mask[tok];
-  float top = 0.0f, sum = 1.0f;
+  uint32_t* keys = s_key[threadIdx.x / L];
+  float top = 0.0f, inv = 0.0f;
   int32_t id = -1;  // of pair `lane`
-  if (live) {
-    float l[V], c[V];
-    load_logits<T, V>(row, e0, a.experts, a.wide, l);
-    settle(l);
-    const bool by_logit = a.softmax && !a.bias && (a.groups == 1 || !a.top2);
-    if (a.softmax && (!by_logit || !a.renormalize)) softmax(l, c, &top, &sum);
-    if (!a.softmax) {
+  float l[V], c[V];
+  load_logits<T, V>(row, e0, a.experts, a.wide, l);
+  if (!in || (a.mask && !a.mask[tok])) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) c[j] = sigmoid(l[j]);
+    for (int j = 0; j < V; ++j) l[j] = -INFINITY;
+  }
+  settle(l);
+  const bool by_logit = a.softmax && !a.bias && (a.groups == 1 || !a.top2);
+  if (a.softmax && (!by_logit || !a.renormalize)) softmax<L, V>(l, c, &top, &inv);
+  if (!a.softmax) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) c[j] = sigmoid(l[j]);
+  }
+  if (by_logit) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) c[j] = l[j];
+  } else {
+    if (a.bias) {
+      float b[V];
+      load_logits<float, V>(a.bias, e0, a.experts, a.wide_bias, b);
+#pragma unroll
+      for (int j = 0; j < V; ++j) c[j] += b[j];
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (by_logit) c[j] = l[j];
-      if (a.bias && e0 + j < a.experts) c[j] += a.bias[e0 + j];
+    for (int j = 0; j < V; ++j)
       if (!(l[j] > -INFINITY) || !(c[j] > -INFINITY)) c[j] = -INFINITY;
-    }
-    if (a.groups > 1) {
-      const uint32_t keep = kept_groups<V>(a, c, reinterpret_cast<float*>(keys), lane);
-      uint32_t g = e0 / a.group_size, r = e0 - g * a.group_size;
+  }
+  if (a.groups > 1) keep_groups<L, V>(a, c, reinterpret_cast<float*>(keys), lane);
+  uint32_t best = 0;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (e0 + j < a.experts && !(keep >> g & 1)) c[j] = -INFINITY;
-        if (++r == a.group_size) r = 0, ++g;
-      }
-    }
-    uint32_t best = 0;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const uint32_t key = order_bits(c[j]);
-      best = max(best, key);
-      keys[e0 + j] = key;
-    }
-    for (uint32_t k = 0; k < a.top_k; ++k) {
-      __syncwarp();
-      const uint32_t m = __reduce_max_sync(kAll, best);
-      if (m == 0) break;
-      const uint32_t from = __ffs(__ballot_sync(kAll, best == m)) - 1;
-      uint32_t x = lane < V ? keys[from * V + lane] : 0;
-      const uint32_t j = __ffs(__ballot_sync(kAll, x == m)) - 1;
-      if (lane == j) {
-        x = 0;
-        keys[from * V + j] = 0;
-      }
-      const uint32_t left = __reduce_max_sync(kAll, x);
-      if (lane == from) best = left;
-      if (lane == k) id = from * V + j;
-    }
+  for (int j = 0; j < V; ++j) {
+    const uint32_t key = order_bits(c[j]);
+    best = max(best, key);
+    keys[e0 + j] = key;
+  }
+  for (uint32_t k = 0; k < a.top_k; ++k) {
+    __syncwarp();
+    const uint32_t m = lanes_max<L>(best);
+    const uint32_t from = first_lane<L>(best == m);
+    const uint32_t x = lane < V ? keys[from * V + lane] : 0;
+    const uint32_t j = first_lane<L>(lane < V && x == m);
+    if (lane == j) keys[from * V + j] = 0;
+    const uint32_t left = lanes_max<L>(lane == j ? 0u : x);
+    if (lane == from) best = left;
+    if (lane == k && m != 0) id = from * V + j;
   }
   // lane k has pair k
-  if (lane >= a.top_k) id = -1;
   float s = 0.0f;
   if (id >= 0) {
-    const float l = fminf(to_float(row[id]), FLT_MAX);
-    s = !a.softmax ? sigmoid(l) : l;
+    s = fminf(to_float(row[id]), FLT_MAX);
+    if (!a.softmax) s = sigmoid(s);
   }
   if (a.softmax) {
-    if (a.renormalize) top = warp_max(id >= 0 ? s : -INFINITY);
+    if (a.renormalize) top = lanes_max<L>(id >= 0 ? s : -INFINITY);
     s = id >= 0 ? expf(s - top) : 0.0f;
-    if (!a.renormalize) s = sum > 0.0f ? s / sum : 0.0f;  // 0: no eligible expert
   }
   if (a.renormalize) {
-    const float all = warp_sum(s);
-    s = all > 0.0f ? s / all : 0.0f;
+    inv = lanes_sum<L>(s);
+    inv = inv > 0.0f ? 1.0f / inv : 0.0f;
   }
-  if (lane < a.top_k) {
-    a.weights[tok * a.top_k + lane] = s * a.scale;
-    a.ids[tok * a.top_k + lane] = id;
+  if (a.softmax || a.renormalize) s *= inv;
+  if (in && lane < a.top_k) {
+    a.weights[(uint64_t)tok * a.top_k + lane] = s * a.scale;
+    a.ids[(uint64_t)tok * a.top_k + lane] = id;
   }
 }
 
@@ -243,56 +272,59 @@ __global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
 // not; then dl_e = u_e - s_e sum u (softmax; the sum is 0 when renormalised)
 // or u_e (1 - s_e) (sigmoid).  Only the softmax without renormalisation has
 // to read the whole row again.  A lane has a pair first, then V experts.
-template <class T, int V>
+template <class T, int L, int V>
 __global__ void __launch_bounds__(kRouteThreads) zc_route_backward_kernel(RouteArgs a) {
-  __shared__ __align__(16) float s_row[kRouteThreads / 32][32 * V];
-  const uint32_t lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-  const uint64_t tok = (uint64_t)blockIdx.x * (kRouteThreads / 32) + wp;
-  if (tok >= a.tokens) return;
-  const T* row = static_cast<const T*>(a.logits) + tok * a.stride;
+  constexpr uint32_t kTok = kRouteThreads / L;
+  __shared__ __align__(16) float s_row[kTok][L * V];
+  const uint32_t lane = threadIdx.x % L;
+  const uint32_t tok = blockIdx.x * kTok + threadIdx.x / L;
+  const bool in = tok < a.tokens;
+  const T* row = static_cast<const T*>(a.logits) + (in ? tok : 0) * a.stride;
+  float* grads = s_row[threadIdx.x / L];
   const uint32_t e0 = lane * V;
   const bool whole = a.softmax && !a.renormalize;
-  int32_t id = lane < a.top_k ? a.ids[tok * a.top_k + lane] : -1;
+  int32_t id = in && lane < a.top_k ? a.ids[(uint64_t)tok * a.top_k + lane] : -1;
   if ((uint32_t)id >= a.experts) id = -1;
   float d = 0.0f, s = 0.0f;
   if (id >= 0) {
-    d = a.grad[tok * a.top_k + lane] * a.scale;
+    d = a.grad[(uint64_t)tok * a.top_k + lane] * a.scale;
     s = fminf(to_float(row[id]), FLT_MAX);
   }
 #pragma unroll
-  for (int j = 0; j < V; ++j) s_row[wp][e0 + j] = 0.0f;
-  float p[V], top = 0.0f, sum = 1.0f;
+  for (int j = 0; j < V; ++j) grads[e0 + j] = 0.0f;
+  float p[V], top = 0.0f, inv = 0.0f;
   if (whole) {
     float l[V];
     load_logits<T, V>(row, e0, a.experts, a.wide, l);
     settle(l);
-    softmax(l, p, &top, &sum);
+    softmax<L, V>(l, p, &top, &inv);
   }
   if (a.softmax) {
-    if (a.renormalize) top = warp_max(id >= 0 ? s : -INFINITY);
+    if (a.renormalize) top = lanes_max<L>(id >= 0 ? s : -INFINITY);
     s = id >= 0 ? expf(s - top) : 0.0f;
-    if (whole) s = sum > 0.0f ? s / sum : 0.0f;
+    if (whole) s *= inv;
   } else if (id >= 0) {
     s = sigmoid(s);
   }
   float u = s * d;
   if (a.renormalize) {
-    const float all = warp_sum(s), w = all > 0.0f ? s / all : 0.0f;
-    u = w * (d - warp_sum(w * d));
+    const float all = lanes_sum<L>(s), w = all > 0.0f ? s * (1.0f / all) : 0.0f;
+    u = w * (d - lanes_sum<L>(w * d));
   }
-  const float total = whole ? warp_sum(u) : 0.0f;
+  const float total = whole ? lanes_sum<L>(u) : 0.0f;
   if (!a.softmax) u *= 1.0f - s;
   __syncwarp();
-  if (id >= 0) atomicAdd(&s_row[wp][id], u);  // a token's ids are distinct: one add each
+  if (id >= 0) atomicAdd(&grads[id], u);  // a token's ids are distinct: one add each
   __syncwarp();
-  T* out = static_cast<T*>(a.grad_logits) + tok * a.experts;
+  if (!in) return;
+  T* out = static_cast<T*>(a.grad_logits) + (uint64_t)tok * a.experts;
   constexpr int N = 16 / sizeof(T) < V ? 16 / sizeof(T) : V;
 #pragma unroll
   for (int j = 0; j < V; j += N) {
     float g[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      g[i] = s_row[wp][e0 + j + i];
+      g[i] = grads[e0 + j + i];
       if (whole) g[i] -= p[j + i] * total;
     }
     if (a.wide_out) {
@@ -305,30 +337,35 @@ __global__ void __launch_bounds__(kRouteThreads) zc_route_backward_kernel(RouteA
   }
 }
 
-template <class T, int V>
+template <class T, int L, int V>
 cudaError_t route_launch(RouteArgs a, bool backward, cudaStream_t s) {
-  constexpr uint32_t kTok = kRouteThreads / 32, N = 16 / sizeof(T) < V ? 16 / sizeof(T) : V;
+  constexpr uint32_t kTok = kRouteThreads / L, N = 16 / sizeof(T) < V ? 16 / sizeof(T) : V, B = V < 4 ? V : 4;
   // accesses of N values: rows of a multiple of N, from an aligned start
   a.wide = host_aligned(a.logits, N * sizeof(T)) && a.stride % N == 0 && a.experts % N == 0;
   a.wide_out = host_aligned(a.grad_logits, N * sizeof(T)) && a.experts % N == 0;
+  a.wide_bias = host_aligned(a.bias, B * sizeof(float)) && a.experts % B == 0;
   const uint32_t lanes = a.group_size % V ? 0 : a.group_size / V;
-  a.group_lanes = lanes & (lanes - 1) ? 0 : lanes;
+  a.group_lanes = lanes & (lanes - 1) || a.groups > L ? 0 : lanes;
   const uint32_t grid = (a.tokens + kTok - 1) / kTok;
   if (backward)
-    zc_route_backward_kernel<T, V><<<grid, kRouteThreads, 0, s>>>(a);
+    zc_route_backward_kernel<T, L, V><<<grid, kRouteThreads, 0, s>>>(a);
   else
-    zc_route_kernel<T, V><<<grid, kRouteThreads, 0, s>>>(a);
+    zc_route_kernel<T, L, V><<<grid, kRouteThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
+// As few lanes as hold the experts 8 at a time, the pairs and the groups.
 template <class T>
 cudaError_t route_by_experts(const RouteArgs& a, bool backward, cudaStream_t s) {
-  if (a.experts <= 32) return route_launch<T, 1>(a, backward, s);
-  if (a.experts <= 64) return route_launch<T, 2>(a, backward, s);
-  if (a.experts <= 128) return route_launch<T, 4>(a, backward, s);
-  if (a.experts <= 256) return route_launch<T, 8>(a, backward, s);
-  if (a.experts <= 512) return route_launch<T, 16>(a, backward, s);
-  return route_launch<T, 32>(a, backward, s);
+  const uint32_t e = a.experts, need = a.top_k > a.groups ? a.top_k : a.groups;
+  if (e <= 64 && need <= 8) return route_launch<T, 8, 8>(a, backward, s);
+  if (e <= 64 && need <= 16) return route_launch<T, 16, 4>(a, backward, s);
+  if (e <= 64) return route_launch<T, 32, 2>(a, backward, s);
+  if (e <= 128 && need <= 16) return route_launch<T, 16, 8>(a, backward, s);
+  if (e <= 128) return route_launch<T, 32, 4>(a, backward, s);
+  if (e <= 256) return route_launch<T, 32, 8>(a, backward, s);
+  if (e <= 512) return route_launch<T, 32, 16>(a, backward, s);
+  return route_launch<T, 32, 32>(a, backward, s);
 }
 
 zipccl_status route(RouteArgs& a, int type, const zipccl_route_options* o, uint64_t tokens, uint32_t experts,
