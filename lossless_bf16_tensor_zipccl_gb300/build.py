@@ -1,7 +1,9 @@
-"""Build libzipccl.so (the sm_103a kernels and the C ABI) in-tree with nvcc.
+"""Build libzipccl.so (the sm_103a kernels and the C ABI) in-tree with nvcc,
+and the extension that makes the operator calls on torch tensors with g++.
 
 Translation units compile in parallel; the shared library lands in
-``lossless_bf16_tensor_zipccl_gb300/_build/libzipccl.so``.
+``lossless_bf16_tensor_zipccl_gb300/_build/libzipccl.so``, the extension beside
+it under a name that holds the Python and torch versions it was built for.
 """
 from __future__ import annotations
 
@@ -66,6 +68,35 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     return LIB
 
 
+def torch_extension(force: bool = False) -> str:
+    """Path of the torch extension, built with g++ when missing or stale."""
+    import sysconfig
+
+    import torch
+    tag = f"{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}"
+    out = os.path.join(BUILD, f"_zipccl_torch.{tag}.so")
+    src = os.path.join(CSRC, "zc_torch.cpp")
+    header = os.path.join(HERE, "..", "include", "zipccl.h")
+    if not force and os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out)
+                                                 for d in (src, header, os.path.abspath(__file__))):
+        return out
+    build()
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda,
+               sysconfig.get_paths()["include"], os.path.dirname(header)]
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *("-I" + i for i in include), src, "-o", tmp, "-L" + BUILD, "-lzipccl", "-Wl,-rpath,$ORIGIN",
+           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-ltorch_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on zc_torch.cpp:\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 if __name__ == "__main__":
     import sys
     print(build(force="--force" in sys.argv, verbose=True, ptxas_info="--ptxas" in sys.argv))
+    print(torch_extension(force="--force" in sys.argv))
