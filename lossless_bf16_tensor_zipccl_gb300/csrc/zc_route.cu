@@ -403,77 +403,102 @@ zipccl_status route(RouteArgs& a, int type, const zipccl_route_options* o, uint6
 }
 
 // ------------------------------------------------------------------ plan
-// A stable counting sort of the pairs by expert.  One block takes kPlanChunk
-// consecutive pairs; with more than one block a first kernel leaves every
-// block's counts in the workspace.
-constexpr int kPlanThreads = 256;
-constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr uint32_t kPlanChunk = 4096;
+// A stable counting sort of the pairs by expert.  A block takes a run of
+// consecutive pairs, a warp of it a run of these.  With more than one block a
+// first kernel leaves the counts of every kPlanGroup blocks in the workspace;
+// the second starts beside it, counts its warps' runs and those of the blocks
+// before it in its group meanwhile, and then adds up, for each bucket, the
+// pairs of the groups before and of all.  524,288 pairs of 256 experts: 9.5 us
+// for both, most of it the chain launch, count, read, place (24 us with a row
+// of counts for every block, of which each block read 131 KB).
+constexpr uint32_t kPlanRun = 2048;    // pairs of a block, or more where that makes
+constexpr uint32_t kPlanBlocks = 128;  // more blocks than this
+constexpr uint32_t kPlanGroup = 4;
+constexpr int kCountThreads = 1024;
+constexpr int kPlaceThreads = 1024;
 
 struct PlanArgs {
   const int32_t* ids;
   int32_t* counts;
   int32_t* offsets;
   int32_t* slots;
-  uint32_t* block_counts;  // [blocks][experts + 1]
-  uint32_t pairs, experts, blocks;
+  uint32_t* group_counts;  // [groups][experts + 1]
+  uint32_t pairs, experts, blocks, run;
 };
 
 // A pair that is not routed (id outside 0..experts-1) counts for one more
 // bucket after the experts.
 __device__ __forceinline__ uint32_t plan_key(int32_t id, uint32_t experts) { return min((uint32_t)id, experts); }
 
-__global__ void __launch_bounds__(kPlanThreads) zc_plan_count_kernel(PlanArgs a) {
+__global__ void __launch_bounds__(kCountThreads) zc_plan_count_kernel(PlanArgs a) {
   __shared__ uint32_t h[kMaxExperts + 1];
-  for (uint32_t e = threadIdx.x; e <= a.experts; e += kPlanThreads) h[e] = 0;
+  // the placing kernel may start: it waits for this one where it needs the counts
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (uint32_t e = threadIdx.x; e <= a.experts; e += kCountThreads) h[e] = 0;
   __syncthreads();
-  const uint32_t lo = blockIdx.x * kPlanChunk, hi = min(lo + kPlanChunk, a.pairs);
-  for (uint32_t i = lo + threadIdx.x; i < hi; i += kPlanThreads) atomicAdd(&h[plan_key(a.ids[i], a.experts)], 1u);
+  const uint32_t lo = blockIdx.x * kPlanGroup * a.run, hi = min(lo + kPlanGroup * a.run, a.pairs);
+#pragma unroll 8
+  for (uint32_t i = lo + threadIdx.x; i < hi; i += kCountThreads) atomicAdd(&h[plan_key(a.ids[i], a.experts)], 1u);
   __syncthreads();
-  for (uint32_t e = threadIdx.x; e <= a.experts; e += kPlanThreads)
-    a.block_counts[(uint64_t)blockIdx.x * (a.experts + 1) + e] = h[e];
+  for (uint32_t e = threadIdx.x; e <= a.experts; e += kCountThreads)
+    a.group_counts[blockIdx.x * (a.experts + 1) + e] = h[e];
 }
 
-__global__ void __launch_bounds__(kPlanThreads) zc_plan_place_kernel(PlanArgs a) {
-  extern __shared__ uint32_t h[];  // [kPlanWarps][buckets], then the totals and the scan's carry
+__global__ void __launch_bounds__(kPlaceThreads) zc_plan_place_kernel(PlanArgs a) {
+  constexpr int kThreads = kPlaceThreads, kWarps = kThreads / 32;
+  extern __shared__ uint32_t h[];  // [kWarps][nb] counts, then places, by warp; [nb] totals, then starts; [nb] places
   const uint32_t nb = a.experts + 1;
-  uint32_t* total = h + kPlanWarps * nb;
-  __shared__ uint32_t s_scan[kPlanWarps];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  for (uint32_t i = threadIdx.x; i < kPlanWarps * nb; i += kPlanThreads) h[i] = 0;
+  uint32_t *start = h + kWarps * nb, *base = start + nb;
+  __shared__ uint32_t s_scan[kWarps];
+  const uint32_t lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  for (uint32_t i = threadIdx.x; i < (kWarps + 2) * nb; i += kThreads) h[i] = 0;
   __syncthreads();
-  // this block's pairs, one run of consecutive pairs for each warp
-  const uint32_t per = kPlanChunk / kPlanWarps;
-  const uint32_t lo = blockIdx.x * kPlanChunk + w * per, hi = min(lo + per, a.pairs);
-  for (uint32_t i = lo + lane; i < hi; i += 32) atomicAdd(&h[w * nb + plan_key(a.ids[i], a.experts)], 1u);
-  __syncthreads();
-  // per bucket: pairs of earlier blocks, and of all
-  for (uint32_t e = threadIdx.x; e < nb; e += kPlanThreads) {
-    uint32_t before = 0, all = 0;
-    if (a.blocks == 1) {
-      for (int v = 0; v < kPlanWarps; ++v) all += h[v * nb + e];
-    } else {
-      for (uint32_t b = 0; b < a.blocks; ++b) {
-        const uint32_t n = a.block_counts[(uint64_t)b * nb + e];
-        if (b < blockIdx.x) before += n;
+  const uint32_t per = a.run / kWarps;  // a multiple of 32
+  const uint32_t lo = blockIdx.x * a.run + w * per;
+  const uint32_t hi = max(lo, min(lo + per, min((blockIdx.x + 1) * a.run, a.pairs)));
+  uint32_t* mine = h + w * nb;
+#pragma unroll 2
+  for (uint32_t i = lo + lane; i < hi; i += 32) atomicAdd(&mine[plan_key(a.ids[i], a.experts)], 1u);
+  if (a.blocks > 1) {
+    const uint32_t group = blockIdx.x / kPlanGroup;
+#pragma unroll 4
+    for (uint32_t i = group * kPlanGroup * a.run + threadIdx.x; i < blockIdx.x * a.run; i += kThreads)
+      atomicAdd(&base[plan_key(a.ids[i], a.experts)], 1u);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the threads of a bucket share the groups
+    const uint32_t groups = (a.blocks + kPlanGroup - 1) / kPlanGroup;
+    const uint32_t wide = (nb + 31) / 32 * 32, parts = max(1u, (uint32_t)kThreads / wide), part = threadIdx.x / wide;
+    for (uint32_t e = threadIdx.x - part * wide; e < nb && part < parts; e += kThreads) {
+      const uint32_t* c = a.group_counts + e;
+      uint32_t before = 0, all = 0;
+#pragma unroll 8
+      for (uint32_t b = part; b < groups; b += parts) {
+        const uint32_t n = c[b * nb];
         all += n;
+        if (b < group) before += n;
       }
-    }
-    total[e] = all;
-    // the warps' counts become where each warp's first pair goes, less the
-    // bucket's start
-    for (int v = 0; v < kPlanWarps; ++v) {
-      const uint32_t n = h[v * nb + e];
-      h[v * nb + e] = before;
-      before += n;
+      atomicAdd(&start[e], all);
+      atomicAdd(&base[e], before);
     }
   }
   __syncthreads();
-  // exclusive scan of the totals, kPlanThreads buckets at a time
+  for (uint32_t e = threadIdx.x; e < nb; e += kThreads) {
+    uint32_t n[kWarps], at = base[e];
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) n[v] = h[v * nb + e];
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) {
+      h[v * nb + e] = at;
+      at += n[v];
+    }
+    if (a.blocks == 1) start[e] = at;
+  }
+  __syncthreads();
+  // starts: exclusive scan of the totals, kThreads buckets at a time
   uint32_t carry = 0;
-  for (uint32_t e0 = 0; e0 < nb; e0 += kPlanThreads) {
+  for (uint32_t e0 = 0; e0 < nb; e0 += kThreads) {
     const uint32_t e = e0 + threadIdx.x;
-    const uint32_t n = e < nb ? total[e] : 0;
+    const uint32_t n = e < nb ? start[e] : 0;
     uint32_t x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -482,35 +507,65 @@ __global__ void __launch_bounds__(kPlanThreads) zc_plan_place_kernel(PlanArgs a)
     }
     if (lane == 31) s_scan[w] = x;
     __syncthreads();
-    uint32_t front = carry, sum = 0;
-    for (int v = 0; v < kPlanWarps; ++v) {
-      if (v < w) front += s_scan[v];
-      sum += s_scan[v];
-    }
-    const uint32_t start = front + x - n;
+    const uint32_t part = lane < kWarps ? s_scan[lane] : 0;
+    const uint32_t first = carry + __reduce_add_sync(kAll, lane < w ? part : 0) + x - n;
     if (e < nb) {
-      for (int v = 0; v < kPlanWarps; ++v) h[v * nb + e] += start;
+      start[e] = first;
       if (blockIdx.x == 0) {
-        a.offsets[e] = (int32_t)start;
+        a.offsets[e] = (int32_t)first;
         if (e < a.experts) a.counts[e] = (int32_t)n;
       }
     }
-    carry += sum;
+    carry += __reduce_add_sync(kAll, part);
     __syncthreads();
   }
-  // places in order: 32 pairs at a time, equal buckets ranked by lane
+  // places in order: 32 pairs at a time, equal buckets ranked by lane.  Lanes
+  // of the same bucket are found bit by bit of its number
+  const uint32_t bits = 32 - __clz(nb);
   for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
     const uint32_t i = i0 + lane;
     const uint32_t key = i < hi ? plan_key(a.ids[i], a.experts) : nb;
-    const unsigned same = __match_any_sync(kAll, key);
+    uint32_t same = kAll;
+#pragma unroll 4
+    for (uint32_t b = 0; b < bits; ++b) {
+      const uint32_t one = 0u - (key >> b & 1);
+      same &= __ballot_sync(kAll, one) ^ ~one;
+    }
     const uint32_t rank = __popc(same & ((1u << lane) - 1));
     uint32_t at = 0;
-    if (key < nb) at = h[w * nb + key] + rank;
+    if (key < nb) at = start[key] + mine[key] + rank;
     __syncwarp();
-    if (key < nb && rank == 0) h[w * nb + key] += __popc(same);
+    if (key < nb && rank == 0) mine[key] += __popc(same);
     __syncwarp();
     if (i < hi) a.slots[i] = key < a.experts ? (int32_t)at : ~(int32_t)at;
   }
+}
+
+// Blocks and their runs: whole warps of 32 pairs for 32 warps.
+void plan_split(uint64_t pairs, uint32_t* blocks, uint32_t* run) {
+  uint64_t r = (pairs + kPlanBlocks - 1) / kPlanBlocks;
+  r = r < kPlanRun ? kPlanRun : (r + 1023) / 1024 * 1024;
+  *run = (uint32_t)r;
+  *blocks = pairs ? (uint32_t)((pairs + r - 1) / r) : 1;
+}
+
+cudaError_t plan_place(const PlanArgs& a, cudaStream_t s) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.blocks);
+  cfg.blockDim = dim3(kPlaceThreads);
+  cfg.dynamicSmemBytes = (kPlaceThreads / 32 + 2) * (a.experts + 1) * sizeof(uint32_t);  // 139 KB for 1,024 experts
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = a.blocks > 1 ? 1 : 0;
+  if (cfg.dynamicSmemBytes > 48000) {
+    const cudaError_t e = cudaFuncSetAttribute(zc_plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&cfg, zc_plan_place_kernel, a);
 }
 
 }  // namespace
@@ -548,8 +603,9 @@ zipccl_status zipccl_moe_route_backward(const float* d_grad_weights, const void*
 
 zipccl_status zipccl_moe_plan_workspace_bytes(uint64_t pairs, uint32_t experts, uint64_t* out_bytes) {
   if (!out_bytes || pairs >= (1ull << 31) || experts == 0 || experts > kMaxExperts) return ZIPCCL_ERR_INVALID_ARG;
-  const uint64_t blocks = (pairs + kPlanChunk - 1) / kPlanChunk;
-  *out_bytes = blocks > 1 ? 4 * blocks * (experts + 1) : 0;
+  uint32_t blocks, run;
+  plan_split(pairs, &blocks, &run);
+  *out_bytes = blocks > 1 ? 4ull * ((blocks + kPlanGroup - 1) / kPlanGroup) * (experts + 1) : 0;
   return ZIPCCL_OK;
 }
 
@@ -568,14 +624,14 @@ zipccl_status zipccl_moe_plan(const int32_t* d_ids, uint64_t pairs, uint32_t exp
   a.counts = d_counts;
   a.offsets = d_offsets;
   a.slots = d_slots;
-  a.block_counts = static_cast<uint32_t*>(d_ws);
+  a.group_counts = static_cast<uint32_t*>(d_ws);
   a.pairs = (uint32_t)pairs;
   a.experts = experts;
-  a.blocks = pairs ? (uint32_t)((pairs + kPlanChunk - 1) / kPlanChunk) : 1;
+  plan_split(pairs, &a.blocks, &a.run);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a.blocks > 1) zc_plan_count_kernel<<<a.blocks, kPlanThreads, 0, s>>>(a);
-  zc_plan_place_kernel<<<a.blocks, kPlanThreads, (kPlanWarps + 1) * (experts + 1) * 4, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? ZIPCCL_OK : ZIPCCL_ERR_CUDA;
+  if (a.blocks > 1) zc_plan_count_kernel<<<(a.blocks + kPlanGroup - 1) / kPlanGroup, kCountThreads, 0, s>>>(a);
+  const cudaError_t e = plan_place(a, s);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ZIPCCL_OK : ZIPCCL_ERR_CUDA;
 }
 
 }  // extern "C"
