@@ -32,30 +32,18 @@ struct RouteArgs {
   bool softmax, renormalize, top2, wide, wide_out, wide_bias;
 };
 
-// Order-preserving bits of a choice score; 0 stands for "cannot be chosen"
-// (-inf and NaN map to it).  -0 counts as +0, so that the two tie.
-__device__ __forceinline__ uint32_t order_bits(float c) {
-  if (!(c > -INFINITY)) return 0;
-  const uint32_t u = __float_as_uint(c + 0.0f);
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
-}
-
 // Over the L lanes of a token, which are consecutive in a warp.
 template <int L>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+__device__ __forceinline__ float lanes_max(float v) {
   if constexpr (L == 32) {
-    return __reduce_max_sync(kAll, v);
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
   } else {
 #pragma unroll
-    for (int o = L / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+    for (int o = L / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
     return v;
   }
-}
-template <int L>
-__device__ __forceinline__ float lanes_max(float v) {
-#pragma unroll
-  for (int o = L / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
 }
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -72,7 +60,7 @@ __device__ __forceinline__ uint32_t first_lane(bool x) {
 }
 
 // The hardware's reciprocal (1 ulp): a score is off by 2 ulp with it, and it
-// takes one instruction where a division takes 10.
+// takes 4 instructions where a division takes 10.
 __device__ __forceinline__ float quick_rcp(float x) {
   float y;
   asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -105,7 +93,7 @@ __device__ __forceinline__ void load_logits(const T* row, uint32_t e0, uint32_t 
 template <int V>
 __device__ __forceinline__ void settle(float (&l)[V]) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) l[j] = l[j] > -INFINITY ? fminf(l[j], FLT_MAX) : -INFINITY;
+  for (int j = 0; j < V; ++j) l[j] = fminf(fmaxf(l[j], -INFINITY), FLT_MAX);  // a maximum leaves NaN out
 }
 template <int L, int V>
 __device__ __forceinline__ void softmax(const float (&l)[V], float (&s)[V], float* top, float* sum) {
@@ -119,7 +107,7 @@ __device__ __forceinline__ void softmax(const float (&l)[V], float (&s)[V], floa
     z += s[j];
   }
   z = lanes_sum<L>(z);
-  const float inv = z > 0.0f ? 1.0f / z : 0.0f;  // 0: no eligible expert
+  const float inv = z > 0.0f ? quick_rcp(z) : 0.0f;  // 0: no eligible expert
 #pragma unroll
   for (int j = 0; j < V; ++j) s[j] *= inv;
   *top = m;
@@ -180,7 +168,7 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, float (&c)[V], f
 }
 
 // L lanes take a token, V consecutive experts each.  The choice scores lie in
-// shared memory as ordered bits; each lane knows the best of its own, and
+// shared memory; each lane knows the best of its own, and
 // top_k times the lanes find the best of these, its place among the V of its
 // lane (the lowest place of the lowest lane is the lowest expert among
 // equals), and what is then best in that lane: no step is one lane's alone.
@@ -190,13 +178,13 @@ template <class T, int L, int V>
 __global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
   static_assert(V <= L, "a lane's experts are scanned by one lane each");
   constexpr uint32_t kTok = kRouteThreads / L;
-  __shared__ __align__(16) uint32_t s_key[kTok][L * V];
+  __shared__ __align__(16) float s_key[kTok][L * V];
   const uint32_t lane = threadIdx.x % L;
   const uint32_t tok = blockIdx.x * kTok + threadIdx.x / L;
   const bool in = tok < a.tokens;
   const T* row = static_cast<const T*>(a.logits) + (in ? tok : 0) * a.stride;
   const uint32_t e0 = lane * V;
-  uint32_t* keys = s_key[threadIdx.x / L];
+  float* keys = s_key[threadIdx.x / L];
   float top = 0.0f, inv = 0.0f;
   int32_t id = -1;  // of pair `lane`
   float l[V], c[V];
@@ -224,26 +212,30 @@ __global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (!(l[j] > -INFINITY) || !(c[j] > -INFINITY)) c[j] = -INFINITY;
+      c[j] = l[j] > -INFINITY ? fmaxf(c[j], -INFINITY) : -INFINITY;
   }
-  if (a.groups > 1) keep_groups<L, V>(a, c, reinterpret_cast<float*>(keys), lane);
-  uint32_t best = 0;
+  if (a.groups > 1) keep_groups<L, V>(a, c, keys, lane);
+  float best = c[0];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const uint32_t key = order_bits(c[j]);
-    best = max(best, key);
-    keys[e0 + j] = key;
+  for (int j = 1; j < V; ++j) best = fmaxf(best, c[j]);
+  constexpr int K = V < 4 ? V : 4;  // stored four at a time: single ones would meet in the same banks
+#pragma unroll
+  for (int j = 0; j < V; j += K) {
+    Pack<float, K> p;
+#pragma unroll
+    for (int i = 0; i < K; ++i) p.v[i] = c[j + i];
+    *reinterpret_cast<Pack<float, K>*>(keys + e0 + j) = p;
   }
   for (uint32_t k = 0; k < a.top_k; ++k) {
     __syncwarp();
-    const uint32_t m = lanes_max<L>(best);
+    const float m = lanes_max<L>(best);
     const uint32_t from = first_lane<L>(best == m);
-    const uint32_t x = lane < V ? keys[from * V + lane] : 0;
+    const float x = lane < V ? keys[from * V + lane] : -INFINITY;
     const uint32_t j = first_lane<L>(lane < V && x == m);
-    if (lane == j) keys[from * V + j] = 0;
-    const uint32_t left = lanes_max<L>(lane == j ? 0u : x);
+    if (lane == j) keys[from * V + j] = -INFINITY;
+    const float left = lanes_max<L>(lane == j ? -INFINITY : x);
     if (lane == from) best = left;
-    if (lane == k && m != 0) id = from * V + j;
+    if (lane == k && m > -INFINITY) id = from * V + j;
   }
   // lane k has pair k
   float s = 0.0f;
@@ -257,7 +249,7 @@ __global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
   }
   if (a.renormalize) {
     inv = lanes_sum<L>(s);
-    inv = inv > 0.0f ? 1.0f / inv : 0.0f;
+    inv = inv > 0.0f ? quick_rcp(inv) : 0.0f;
   }
   if (a.softmax || a.renormalize) s *= inv;
   if (in && lane < a.top_k) {
@@ -308,7 +300,7 @@ __global__ void __launch_bounds__(kRouteThreads) zc_route_backward_kernel(RouteA
   }
   float u = s * d;
   if (a.renormalize) {
-    const float all = lanes_sum<L>(s), w = all > 0.0f ? s * (1.0f / all) : 0.0f;
+    const float all = lanes_sum<L>(s), w = all > 0.0f ? s * quick_rcp(all) : 0.0f;
     u = w * (d - lanes_sum<L>(w * d));
   }
   const float total = whole ? lanes_sum<L>(u) : 0.0f;
