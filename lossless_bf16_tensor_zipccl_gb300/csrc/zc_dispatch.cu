@@ -176,6 +176,48 @@ __device__ __forceinline__ uint4 shared16_shifted(uint32_t at) {
   return v;
 }
 
+// The same where it is known which words and halves of words are wanted.
+template <int kWord, int kHalf>
+__device__ __forceinline__ uint4 shared16_at(uint32_t from) {
+  const uint2 p = shared8(from), q = shared8(from + 8);
+  if constexpr (!kWord && !kHalf) return make_uint4(p.x, p.y, q.x, q.y);
+  const uint2 r = shared8(from + 16);
+  const uint32_t w[6] = {p.x, p.y, q.x, q.y, r.x, r.y};
+  if constexpr (!kHalf) return make_uint4(w[1], w[2], w[3], w[4]);
+  return make_uint4(__funnelshift_r(w[kWord], w[kWord + 1], 16), __funnelshift_r(w[kWord + 1], w[kWord + 2], 16),
+                    __funnelshift_r(w[kWord + 2], w[kWord + 3], 16), __funnelshift_r(w[kWord + 3], w[kWord + 4], 16));
+}
+
+// Calls f(h, the 16 bytes at shared address at + h * step) for h < V; `at` is a
+// multiple of 2, and its place within 8 the same for a whole warp if kWarp
+// (one branch then takes the place of selecting every word).
+template <int V, bool kWarp, class F>
+__device__ __forceinline__ void each_shifted(uint32_t at, uint32_t step, F f) {
+  if constexpr (!kWarp) {
+#pragma unroll
+    for (int h = 0; h < V; ++h) f(h, shared16_shifted(at + h * step));
+  } else {
+    const uint32_t from = at & ~7u;
+    switch (at >> 1 & 3) {
+      case 0:
+#pragma unroll
+        for (int h = 0; h < V; ++h) f(h, shared16_at<0, 0>(from + h * step));
+        break;
+      case 1:
+#pragma unroll
+        for (int h = 0; h < V; ++h) f(h, shared16_at<0, 1>(from + h * step));
+        break;
+      case 2:
+#pragma unroll
+        for (int h = 0; h < V; ++h) f(h, shared16_at<1, 0>(from + h * step));
+        break;
+      default:
+#pragma unroll
+        for (int h = 0; h < V; ++h) f(h, shared16_at<1, 1>(from + h * step));
+    }
+  }
+}
+
 template <class T>
 using Vec = Pack<T, 16 / sizeof(T)>;
 
@@ -234,7 +276,7 @@ template <class T, int V, bool kOdd>
 __global__ void __launch_bounds__(kPipeThreads) zc_combine_pipe_kernel(RowArgs a, Pipe q) {
   constexpr int N = 16 / sizeof(T), R = kStageVec / V;  // rows of a stage
   extern __shared__ __align__(16) uint8_t ring[];
-  const uint32_t lanes = 1u << q.log_lanes, lane = threadIdx.x & (lanes - 1);
+  const uint32_t lanes = V > 1 ? 32 : 1u << q.log_lanes, lane = threadIdx.x & (lanes - 1);
   const uint32_t row_stage = (lanes * V + (kOdd ? 1 : 0)) * 16, group_stage = row_stage * R;
   const uint32_t groups = gridDim.x * kPipeThreads >> q.log_lanes;
   const uint32_t group = (blockIdx.x * kPipeThreads + threadIdx.x) >> q.log_lanes;
@@ -327,11 +369,16 @@ __global__ void __launch_bounds__(kPipeThreads) zc_combine_pipe_kernel(RowArgs a
       for (int j = 0; j < R; ++j) {
         if (!ok[j]) continue;
         const uint32_t at = stage + j * row_stage + 16 * lane + (kOdd ? (row[j] * q.bytes - shift) & 15 : 0);
-#pragma unroll
-        for (int h = 0; h < V; ++h) {
-          const Vec<T> p = as_vec<T>(kOdd ? shared16_shifted(at + 16 * h * lanes) : shared16(at + 16 * h * lanes));
+        auto add = [&](int h, uint4 v) {
+          const Vec<T> p = as_vec<T>(v);
 #pragma unroll
           for (int i = 0; i < N; ++i) y[h][i] = fmaf(w[j], to_float(p.v[i]), y[h][i]);
+        };
+        if constexpr (kOdd) {
+          each_shifted<V, (V > 1)>(at, 16 * lanes, add);
+        } else {
+#pragma unroll
+          for (int h = 0; h < V; ++h) add(h, shared16(at + 16 * h * lanes));
         }
       }
       copy_next();
@@ -359,7 +406,7 @@ __global__ void __launch_bounds__(kPipeThreads) zc_combine_backward_pipe_kernel(
   constexpr int N = 16 / sizeof(T), R = kStageVec / V;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float s_sum[kOpenRows][kPipeWarps][kMaxTopK];
-  const uint32_t lanes = 1u << q.log_lanes, lane = threadIdx.x & (lanes - 1);
+  const uint32_t lanes = V > 1 ? 32 : 1u << q.log_lanes, lane = threadIdx.x & (lanes - 1);
   const uint32_t row_stage = (lanes * V + (kOdd ? 2 : 0)) * 16, group_stage = row_stage * R;
   const uint32_t groups = gridDim.x * kPipeThreads >> q.log_lanes;
   const uint32_t group = (blockIdx.x * kPipeThreads + threadIdx.x) >> q.log_lanes;
@@ -507,14 +554,17 @@ __global__ void __launch_bounds__(kPipeThreads) zc_combine_backward_pipe_kernel(
             const uint32_t shift = kOdd ? row * q.bytes & 15 : 0;
             const uint32_t own = stage + j * row_stage + 16 * lane;
             T* out = static_cast<T*>(a.dst) + (uint64_t)row * a.hidden;
+            const int32_t e0 = (int32_t)((first + lane) * N) - (int32_t)(shift / sizeof(T)), step = (int32_t)lanes * N;
+            if (s[j] < 0) {
 #pragma unroll
-            for (int h = 0; h < V; ++h) {
-              const int32_t e = (int32_t)((first + h * lanes + lane) * N) - (int32_t)(shift / sizeof(T));
-              if (e >= hidden) break;
-              Vec<T> o = as_vec<T>(make_uint4(0, 0, 0, 0));
-              if (s[j] >= 0) {
-                if (kOdd) {
-                  const Vec<T> g = as_vec<T>(shared16_shifted(row_at + e * (int32_t)sizeof(T)));
+              for (int h = 0; h < V; ++h)
+                if (e0 + h * step < hidden) put<T, kOdd>(out, as_vec<T>(make_uint4(0, 0, 0, 0)), e0 + h * step, hidden);
+            } else {
+              auto take = [&](int h, uint4 g16) {
+                const int32_t e = e0 + h * step;
+                if (e >= hidden) return;
+                if constexpr (kOdd) {
+                  const Vec<T> g = as_vec<T>(g16);
 #pragma unroll
                   for (int i = 0; i < N; ++i) x[h][i] = to_float(g.v[i]);
                 }
@@ -530,9 +580,14 @@ __global__ void __launch_bounds__(kPipeThreads) zc_combine_backward_pipe_kernel(
                 float z[N];
 #pragma unroll
                 for (int i = 0; i < N; ++i) z[i] = w[j] * x[h][i];
-                o = rounded<T, N>(z);
+                put<T, kOdd>(out, rounded<T, N>(z), e, hidden);
+              };
+              if constexpr (kOdd) {
+                each_shifted<V, (V > 1)>(row_at + e0 * (int32_t)sizeof(T), 16 * lanes, take);
+              } else {
+#pragma unroll
+                for (int h = 0; h < V; ++h) take(h, uint4{});
               }
-              put<T, kOdd>(out, o, e, hidden);
             }
           }
           if (grads) {
@@ -572,7 +627,7 @@ template <class T, int V>
 __global__ void __launch_bounds__(kPipeThreads) zc_dispatch_odd_kernel(RowArgs a, Pipe q) {
   constexpr int N = 16 / sizeof(T), S = 2;
   extern __shared__ __align__(16) uint8_t ring[];
-  const uint32_t lanes = 1u << q.log_lanes, lane = threadIdx.x & (lanes - 1);
+  const uint32_t lanes = V > 1 ? 32 : 1u << q.log_lanes, lane = threadIdx.x & (lanes - 1);
   const uint32_t group_stage = (lanes * V + 4) * 16;  // a unit in front: reads of a row's first vector start there
   const uint32_t groups = gridDim.x * kPipeThreads >> q.log_lanes;
   const uint32_t group = (blockIdx.x * kPipeThreads + threadIdx.x) >> q.log_lanes;
@@ -607,13 +662,15 @@ __global__ void __launch_bounds__(kPipeThreads) zc_dispatch_odd_kernel(RowArgs a
         if ((uint64_t)row >= a.rows) continue;
         const int64_t shift = (int64_t)((uint64_t)row * q.bytes & 15);
         T* out = static_cast<T*>(a.dst) + row * hidden;
+        const int32_t e0 = (int32_t)((first + lane) * N - shift / (int64_t)sizeof(T)), step = (int32_t)lanes * N;
+        auto give = [&](int h, uint4 v) {
+          if (e0 + h * step < (int32_t)hidden) put<T, true>(out, as_vec<T>(v), e0 + h * step, (int32_t)hidden);
+        };
+        if (s < 0) {
 #pragma unroll
-        for (int h = 0; h < V; ++h) {
-          const int64_t e = (first + h * lanes + lane) * N - shift / (int64_t)sizeof(T);
-          if (e >= hidden) break;
-          Vec<T> o = as_vec<T>(make_uint4(0, 0, 0, 0));
-          if (s >= 0) o = as_vec<T>(shared16_shifted((uint32_t)((int64_t)from + e * (int64_t)sizeof(T) - kept0)));
-          put<T, true>(out, o, (int32_t)e, (int32_t)hidden);
+          for (int h = 0; h < V; ++h) give(h, make_uint4(0, 0, 0, 0));
+        } else {
+          each_shifted<V, (V > 1)>((uint32_t)((int64_t)from + e0 * (int64_t)sizeof(T) - kept0), 16 * lanes, give);
         }
       }
     }
@@ -694,8 +751,13 @@ template <class T, bool kOdd>
 cudaError_t pipe_by_width(RowOp op, const RowArgs& a, cudaStream_t s) {
   // vectors of a row: one more where it may start within one
   const uint64_t vectors = (a.hidden * sizeof(T) + 15) / 16 + (kOdd ? 1 : 0);
-  if (vectors > 64) return pipe_form<T, 4, kOdd>(op, a, 5, vectors, s);
-  if (vectors > 32) return pipe_form<T, 2, kOdd>(op, a, 5, vectors, s);
+  if (vectors > 32) {
+    // vectors of a lane, 4 to 2: those that leave the fewest places of a row's pieces empty
+    const auto places = [&](uint64_t v) { return (vectors + 32 * v - 1) / (32 * v) * v; };
+    if (places(4) <= places(3) && places(4) <= places(2)) return pipe_form<T, 4, kOdd>(op, a, 5, vectors, s);
+    if (places(3) <= places(2)) return pipe_form<T, 3, kOdd>(op, a, 5, vectors, s);
+    return pipe_form<T, 2, kOdd>(op, a, 5, vectors, s);
+  }
   uint32_t log_lanes = 2;
   while ((1u << log_lanes) < vectors) ++log_lanes;
   return pipe_form<T, 1, kOdd>(op, a, log_lanes, vectors, s);
