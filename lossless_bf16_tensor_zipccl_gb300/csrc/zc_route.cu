@@ -247,11 +247,12 @@ __global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
     if (a.renormalize) top = lanes_max<L>(id >= 0 ? s : -INFINITY);
     s = id >= 0 ? expf(s - top) : 0.0f;
   }
-  if (a.renormalize) {
-    inv = lanes_sum<L>(s);
-    inv = inv > 0.0f ? quick_rcp(inv) : 0.0f;
+  if (a.renormalize) {  // a division: a single pair's weight is 1, and its gradient 0
+    const float all = lanes_sum<L>(s);
+    s = all > 0.0f ? s / all : 0.0f;
+  } else if (a.softmax) {
+    s *= inv;
   }
-  if (a.softmax || a.renormalize) s *= inv;
   if (in && lane < a.top_k) {
     a.weights[(uint64_t)tok * a.top_k + lane] = s * a.scale;
     a.ids[(uint64_t)tok * a.top_k + lane] = id;
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kRouteThreads) zc_route_backward_kernel(RouteA
   }
   float u = s * d;
   if (a.renormalize) {
-    const float all = lanes_sum<L>(s), w = all > 0.0f ? s * quick_rcp(all) : 0.0f;
+    const float all = lanes_sum<L>(s), w = all > 0.0f ? s / all : 0.0f;
     u = w * (d - lanes_sum<L>(w * d));
   }
   const float total = whole ? lanes_sum<L>(u) : 0.0f;

@@ -209,6 +209,16 @@ def test_route_strides_streams_and_given_outputs():
         assert torch.equal(zc.moe_route_backward(g, part, ids), zc.moe_route_backward(g, part.contiguous(), ids))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [5, 64, 128, 256])
+def test_route_of_one_renormalised_pair_is_exact(score, E):
+    torch.manual_seed(E)
+    l = torch.randn(500, E, device="cuda")
+    w, ids = zc.moe_route(l, 1, score=score, scale=2.5)
+    assert (w == 2.5).all() and torch.equal(ids[:, 0].long(), l.argmax(1))
+    assert not zc.moe_route_backward(torch.randn(500, 1, device="cuda"), l, ids, score=score, scale=2.5).any()
+
+
 def test_route_no_tokens():
     w, ids = zc.moe_route(torch.zeros(0, 64, device="cuda"), 2)
     assert w.shape == ids.shape == (0, 2)
