@@ -228,17 +228,45 @@ __device__ __forceinline__ Vec<T> as_vec(uint4 v) {
   return x.p;
 }
 
-// A vector of a row of `hidden` values whose first value has place `first`.
+// A vector of a row of `hidden` values whose first value has place `first`.  Its
+// values outside the row are not written: that is a function of its own, for
+// the code around each vector to stay small.
+template <class T>
+__device__ __noinline__ void put_edge(T* row, uint4 v, int32_t first, int32_t hidden) {
+  constexpr int N = 16 / sizeof(T);
+  const Vec<T> o = as_vec<T>(v);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (first + i >= 0 && first + i < hidden) row[first + i] = o.v[i];
+}
+template <class T>
+__device__ __forceinline__ uint4 as_words(const Vec<T>& v) {
+  union { Vec<T> p; uint4 u; } x;
+  x.p = v;
+  return x.u;
+}
 template <class T, bool kOdd>
 __device__ __forceinline__ void put(T* row, const Vec<T>& o, int32_t first, int32_t hidden) {
   constexpr int N = 16 / sizeof(T);
-  if (!kOdd || (first >= 0 && first + N <= hidden)) {
+  if (!kOdd || (first >= 0 && first + N <= hidden))
     *reinterpret_cast<Vec<T>*>(row + first) = o;
-  } else {
+  else
+    put_edge<T>(row, as_words<T>(o), first, hidden);
+}
+
+// The gradient's row and the product's part of such a vector.
+template <class T>
+__device__ __noinline__ float take_edge(T* row, uint4 grad, uint4 value, float w, int32_t first, int32_t hidden) {
+  constexpr int N = 16 / sizeof(T);
+  const Vec<T> g = as_vec<T>(grad), p = as_vec<T>(value);
+  float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (first + i >= 0 && first + i < hidden) row[first + i] = o.v[i];
-  }
+  for (int i = 0; i < N; ++i)
+    if (first + i >= 0 && first + i < hidden) {
+      dot = fmaf(to_float(g.v[i]), to_float(p.v[i]), dot);
+      row[first + i] = from_float<T>(w * to_float(g.v[i]));
+    }
+  return dot;
 }
 
 // What the piped kernels work with: groups of `lanes` lanes take pieces of
@@ -563,24 +591,24 @@ __global__ void __launch_bounds__(kPipeThreads) zc_combine_backward_pipe_kernel(
               auto take = [&](int h, uint4 g16) {
                 const int32_t e = e0 + h * step;
                 if (e >= hidden) return;
+                const uint4 p16 = shared16(own + 16 * h * lanes);
+                if (kOdd && (e < 0 || e + N > hidden)) {
+                  dot += take_edge<T>(out, g16, p16, w[j], e, hidden);
+                  return;
+                }
                 if constexpr (kOdd) {
                   const Vec<T> g = as_vec<T>(g16);
 #pragma unroll
                   for (int i = 0; i < N; ++i) x[h][i] = to_float(g.v[i]);
                 }
-                const Vec<T> p = as_vec<T>(shared16(own + 16 * h * lanes));
-                if (!kOdd || (e >= 0 && e + N <= hidden)) {
-#pragma unroll
-                  for (int i = 0; i < N; ++i) dot = fmaf(x[h][i], to_float(p.v[i]), dot);
-                } else {
-#pragma unroll
-                  for (int i = 0; i < N; ++i)
-                    if (e + i >= 0 && e + i < hidden) dot = fmaf(x[h][i], to_float(p.v[i]), dot);
-                }
+                const Vec<T> p = as_vec<T>(p16);
                 float z[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) z[i] = w[j] * x[h][i];
-                put<T, kOdd>(out, rounded<T, N>(z), e, hidden);
+                for (int i = 0; i < N; ++i) {
+                  dot = fmaf(x[h][i], to_float(p.v[i]), dot);
+                  z[i] = w[j] * x[h][i];
+                }
+                *reinterpret_cast<Vec<T>*>(out + e) = rounded<T, N>(z);
               };
               if constexpr (kOdd) {
                 each_shifted<V, (V > 1)>(row_at + e0 * (int32_t)sizeof(T), 16 * lanes, take);
