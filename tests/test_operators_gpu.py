@@ -547,3 +547,86 @@ def test_adamw_past_32_bits():
     assert torch.equal(p[-tail:], pt) and not torch.equal(pt, torch.zeros_like(pt))
     assert torch.equal(m.view(torch.uint8)[-tail:], st[0].view(torch.uint8))
     assert torch.equal(vs[-4:], st[3]) and not p[:256].any()
+
+
+# ------------------------------------------------------------------ graphs, the pointer-level calls
+def test_calls_capture_into_a_cuda_graph_and_replay():
+    """Captured once, replayed with new values in the same buffers: what the
+    calls give outside a graph."""
+    T, E, k, H = 3000, 64, 4, 264
+    torch.manual_seed(6)
+    logits, x = torch.randn(T, E, device="cuda"), torch.randn(T, H, device="cuda").bfloat16()
+    p, g = torch.randn(5000, device="cuda"), torch.randn(5000, device="cuda").bfloat16()
+    m, v, ms, vs = zc.adamw_state(p, bits=8)
+
+    def step():
+        w, ids = zc.moe_route(logits, k, score="sigmoid")
+        plan = zc.moe_plan(ids, E)
+        rows = zc.moe_dispatch(x, plan.slots)
+        y = zc.moe_combine(rows, plan.slots, w)
+        gr, gw = zc.moe_combine_backward(y, rows, plan.slots, w)
+        gx = zc.moe_dispatch_backward(gr, plan.slots)
+        gl = zc.moe_route_backward(gw, logits, ids, score="sigmoid")
+        zc.adamw_step([p], [g], [m], [v], scales=([ms], [vs]), step=2, lr=1e-2)
+        return [w, ids, *plan, rows, y, gr, gw, gx, gl]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                                # each call once before capturing
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for seed in (1, 2):
+        torch.manual_seed(seed)
+        logits.copy_(torch.randn(T, E, device="cuda"))
+        x.copy_(torch.randn(T, H, device="cuda"))
+        g.copy_(torch.randn(5000, device="cuda"))
+        before = [t.clone() if t.dtype != torch.float8_e4m3fn else t.view(torch.uint8).clone() for t in (p, m, v, ms, vs)]
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in captured] + [p.clone(), m.view(torch.uint8).clone(), ms.clone()]
+        for t, b in zip((p, m, v, ms, vs), before):
+            (t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t).copy_(b)
+        want = step() + [p, m.view(torch.uint8), ms]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_pointer_level_calls_match_the_tensor_level():
+    T, E, k, H = 200, 32, 2, 96
+    torch.manual_seed(8)
+    s = torch.cuda.current_stream().cuda_stream
+    logits, x = torch.randn(T, E, device="cuda"), torch.randn(T, H, device="cuda").bfloat16()
+    w, ids = torch.empty(T, k, device="cuda"), torch.empty(T, k, dtype=torch.int32, device="cuda")
+    opt = zc.RouteOptions(k, 0, 1, 1.0, 1, 1, 0)
+    assert zc.zipccl_moe_route(logits.data_ptr(), zc.TYPE_F32, E, T, E, opt, 0, 0, w.data_ptr(), ids.data_ptr(), s) == zc.OK
+    w2, ids2 = zc.moe_route(logits, k)
+    assert torch.equal(w, w2) and torch.equal(ids, ids2)
+    counts, offsets = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (E, E + 1))
+    slots = torch.empty_like(ids)
+    assert zc.zipccl_moe_plan(ids.data_ptr(), T * k, E, counts.data_ptr(), offsets.data_ptr(), slots.data_ptr(), 0, 0, s) == zc.OK
+    assert all(torch.equal(a, b) for a, b in zip(zc.moe_plan(ids, E), (counts, offsets, slots)))
+    rows, y = torch.empty(T * k, H, dtype=x.dtype, device="cuda"), torch.empty_like(x)
+    assert zc.zipccl_moe_dispatch(x.data_ptr(), zc.TYPE_BF16, H, T, k, H, slots.data_ptr(), rows.data_ptr(), s) == zc.OK
+    assert torch.equal(rows, zc.moe_dispatch(x, slots))
+    assert zc.zipccl_moe_combine(rows.data_ptr(), zc.TYPE_BF16, T, k, H, slots.data_ptr(), w.data_ptr(), x.data_ptr(),
+                                 y.data_ptr(), s) == zc.OK
+    assert torch.equal(y, zc.moe_combine(rows, slots, w, residual=x))
+    gr, gw, gx, gl = torch.empty_like(rows), torch.empty_like(w), torch.empty_like(x), torch.empty_like(logits)
+    assert zc.zipccl_moe_combine_backward(y.data_ptr(), rows.data_ptr(), zc.TYPE_BF16, T, k, H, slots.data_ptr(),
+                                          w.data_ptr(), gr.data_ptr(), gw.data_ptr(), s) == zc.OK
+    assert zc.zipccl_moe_dispatch_backward(gr.data_ptr(), zc.TYPE_BF16, T, k, H, slots.data_ptr(), gx.data_ptr(), s) == zc.OK
+    assert zc.zipccl_moe_route_backward(gw.data_ptr(), logits.data_ptr(), zc.TYPE_F32, E, T, E, opt, ids.data_ptr(),
+                                        gl.data_ptr(), s) == zc.OK
+    a, b = zc.moe_combine_backward(y, rows, slots, w)
+    assert torch.equal(gr, a) and torch.equal(gw, b) and torch.equal(gx, zc.moe_dispatch_backward(gr, slots))
+    assert torch.equal(gl, zc.moe_route_backward(gw, logits, ids))
+    p = torch.randn(700, device="cuda")
+    q, m, v = p.clone(), torch.zeros(700, device="cuda"), torch.zeros(700, device="cuda")
+    g = p.clone()
+    record = (zc.AdamWTensor * 1)(zc.AdamWTensor(d_param=p.data_ptr(), d_grad=g.data_ptr(), d_exp_avg=m.data_ptr(),
+                                                 d_exp_avg_sq=v.data_ptr(), n=700))
+    assert zc.zipccl_adamw_step(record, 1, zc.TYPE_F32, zc.TYPE_F32, 32, zc.AdamWOptions(1e-3, 0.9, 0.99, 1e-8, 0.1, 1), 0, s) == zc.OK
+    zc.adamw_step([q], [g], [torch.zeros_like(m)], [torch.zeros_like(v)], step=1, lr=1e-3, betas=(0.9, 0.99), weight_decay=0.1)
+    assert torch.equal(p, q) and m.any()
