@@ -168,12 +168,14 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, float (&c)[V], f
 }
 
 // L lanes take a token, V consecutive experts each.  The choice scores lie in
-// shared memory; each lane knows the best of its own, and
-// top_k times the lanes find the best of these, its place among the V of its
-// lane (the lowest place of the lowest lane is the lowest expert among
-// equals), and what is then best in that lane: no step is one lane's alone.
-// It is bound by its instructions: 16,384 tokens of 64 experts took 389 a token
-// with all of a warp's lanes, as against L = 8.
+// shared memory; each lane knows the best of its own, and top_k times the
+// lanes find the best of these, its place among the V of its lane (the lowest
+// place of the lowest lane is the lowest expert among equals), and what is
+// then best in that lane: no step is one lane's alone.
+// For few tokens it takes a launch (2.6 us); for many its instructions bound
+// it: of 256 experts in 8 groups, 8 chosen, a token takes 826, 29 of them for
+// each chosen expert, 158 for the sigmoids, 166 for the groups (8,192 tokens:
+// 8.5 us; 32,768: 26.8 us, 1.3 TB/s).
 template <class T, int L, int V>
 __global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
   static_assert(V <= L, "a lane's experts are scanned by one lane each");
@@ -347,14 +349,15 @@ cudaError_t route_launch(RouteArgs a, bool backward, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// As few lanes as hold the experts 8 at a time, the pairs and the groups.
+// A warp takes a token; 8 lanes do where they hold its experts, 8 each, its
+// pairs and its groups: 16,384 tokens of 64 experts, two chosen, 3.4 us against
+// 5.6 with 32 lanes, one token 2.6 against 2.3.  (Between 65 and 128 experts 16
+// lanes made no difference, nor did they up to 256.)
 template <class T>
 cudaError_t route_by_experts(const RouteArgs& a, bool backward, cudaStream_t s) {
-  const uint32_t e = a.experts, need = a.top_k > a.groups ? a.top_k : a.groups;
-  if (e <= 64 && need <= 8) return route_launch<T, 8, 8>(a, backward, s);
-  if (e <= 64 && need <= 16) return route_launch<T, 16, 4>(a, backward, s);
+  const uint32_t e = a.experts;
+  if (e <= 64 && a.top_k <= 8 && a.groups <= 8) return route_launch<T, 8, 8>(a, backward, s);
   if (e <= 64) return route_launch<T, 32, 2>(a, backward, s);
-  if (e <= 128 && need <= 16) return route_launch<T, 16, 8>(a, backward, s);
   if (e <= 128) return route_launch<T, 32, 4>(a, backward, s);
   if (e <= 256) return route_launch<T, 32, 8>(a, backward, s);
   if (e <= 512) return route_launch<T, 32, 16>(a, backward, s);
