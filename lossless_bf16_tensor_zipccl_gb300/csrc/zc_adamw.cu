@@ -222,6 +222,7 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const StepTensor& 
 
 template <class P, class G, bool k8>
 __global__ void __launch_bounds__(kStepThreads, kStepBlocks<k8>) zc_adamw_kernel(const __grid_constant__ StepArgs a) {
+  after_previous();
   // the tensor of this tile
   uint32_t lo = 0, hi = a.count;
   while (hi - lo > 1) {
@@ -239,12 +240,9 @@ __global__ void __launch_bounds__(kStepThreads, kStepBlocks<k8>) zc_adamw_kernel
 }
 
 template <class P, class G>
-void step_launch(const StepArgs& a, bool k8, cudaStream_t s) {
+cudaError_t step_launch(const StepArgs& a, bool k8, cudaStream_t s) {
   const uint32_t tiles = a.tile[a.count];
-  if (k8)
-    zc_adamw_kernel<P, G, true><<<tiles, kStepThreads, 0, s>>>(a);
-  else
-    zc_adamw_kernel<P, G, false><<<tiles, kStepThreads, 0, s>>>(a);
+  return launch(k8 ? zc_adamw_kernel<P, G, true> : zc_adamw_kernel<P, G, false>, tiles, kStepThreads, 0, s, a);
 }
 
 }  // namespace
@@ -305,11 +303,10 @@ extern "C" zipccl_status zipccl_adamw_step(const zipccl_adamw_tensor* tensors, u
     }
     if (a.count == 0) break;
     a.tile[a.count] = (uint32_t)tiles;
-    if (pf && gf) step_launch<float, float>(a, k8, s);
-    else if (pf) step_launch<float, __nv_bfloat16>(a, k8, s);
-    else if (gf) step_launch<__nv_bfloat16, float>(a, k8, s);
-    else step_launch<__nv_bfloat16, __nv_bfloat16>(a, k8, s);
-    if (cudaGetLastError() != cudaSuccess) return ZIPCCL_ERR_CUDA;
+    const cudaError_t e = pf ? gf ? step_launch<float, float>(a, k8, s) : step_launch<float, __nv_bfloat16>(a, k8, s)
+                             : gf ? step_launch<__nv_bfloat16, float>(a, k8, s)
+                                  : step_launch<__nv_bfloat16, __nv_bfloat16>(a, k8, s);
+    if (e != cudaSuccess) return ZIPCCL_ERR_CUDA;
   }
   return ZIPCCL_OK;
 }

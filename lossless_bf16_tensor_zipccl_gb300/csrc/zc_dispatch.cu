@@ -53,6 +53,7 @@ struct RowArgs {
 // moved as they are: W is any type of a vector's size.
 template <class W>
 __global__ void __launch_bounds__(kRowThreads) zc_dispatch_kernel(RowArgs a, uint64_t stride, uint64_t nv) {
+  after_previous();
   const uint64_t t = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= a.tokens) return;
   const int32_t* slots = a.slots + t * a.top_k;
@@ -72,6 +73,7 @@ __global__ void __launch_bounds__(kRowThreads) zc_dispatch_kernel(RowArgs a, uin
 // order, held in 32 bits and rounded once.
 template <class T>
 __global__ void __launch_bounds__(kRowThreads) zc_combine_kernel(RowArgs a) {
+  after_previous();
   const uint64_t t = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= a.tokens) return;
   const int32_t* slots = a.slots + t * a.top_k;
@@ -93,6 +95,7 @@ __global__ void __launch_bounds__(kRowThreads) zc_combine_kernel(RowArgs a) {
 // The products are summed along a fixed tree: a thread's, lanes, warps.
 template <class T>
 __global__ void __launch_bounds__(kRowThreads) zc_combine_backward_kernel(RowArgs a) {
+  after_previous();
   __shared__ float s_dot[kRowThreads / 32];
   const uint64_t t = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = t < a.tokens;
@@ -721,12 +724,8 @@ cudaError_t plain_launch(RowOp op, const RowArgs& a, cudaStream_t s) {
   const dim3 block = row_block(a.hidden / kN);
   const uint32_t grid = (a.tokens + block.y - 1) / block.y;
   if (op == RowOp::kDispatch)
-    zc_dispatch_kernel<Pack<T, kN>><<<grid, block, 0, s>>>(a, a.stride / kN, a.hidden / kN);
-  else if (op == RowOp::kCombine)
-    zc_combine_kernel<T><<<grid, block, 0, s>>>(a);
-  else
-    zc_combine_backward_kernel<T><<<grid, block, 0, s>>>(a);
-  return cudaGetLastError();
+    return launch(zc_dispatch_kernel<Pack<T, kN>>, grid, block, 0, s, a, a.stride / kN, a.hidden / kN);
+  return launch(op == RowOp::kCombine ? zc_combine_kernel<T> : zc_combine_backward_kernel<T>, grid, block, 0, s, a);
 }
 
 // A persistent launch: as many blocks as the device holds at once (looked up
@@ -751,6 +750,9 @@ cudaError_t pipe_launch(const RowArgs& a, const Pipe& q, uint64_t items, uint32_
   // as few blocks as take no more turns: all have the same number of items
   const uint64_t groups = kPipeThreads >> q.log_lanes, want = (items + groups - 1) / groups;
   const uint64_t turns = (want + blocks - 1) / blocks;
+  // not through launch(): blocks that start where room first appears lie
+  // unevenly, and a persistent block stays where it started (200 us for combine
+  // and its gradient, 165 like this)
   kKernel<<<(uint32_t)((want + turns - 1) / turns), kPipeThreads, smem, s>>>(a, q);
   return cudaGetLastError();
 }

@@ -64,6 +64,31 @@ __device__ __forceinline__ Pack<__half, 8> rounded<__half, 8>(const float (&x)[8
   return p;
 }
 
+// A kernel that is launched by launch() begins with after_previous(): it may be
+// set up while the kernel before it in the stream still runs.  Its blocks start
+// as that one's last blocks leave room and wait here, before they touch memory,
+// until it has ended and its writes are visible.  Calls back to back lose 1 to
+// 2 us less between them.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 inline bool host_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 inline uint32_t type_bytes(int type) {

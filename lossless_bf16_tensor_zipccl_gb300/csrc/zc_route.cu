@@ -179,6 +179,7 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, float (&c)[V], f
 template <class T, int L, int V>
 __global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
   static_assert(V <= L, "a lane's experts are scanned by one lane each");
+  after_previous();
   constexpr uint32_t kTok = kRouteThreads / L;
   __shared__ __align__(16) float s_key[kTok][L * V];
   const uint32_t lane = threadIdx.x % L;
@@ -269,6 +270,7 @@ __global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
 // to read the whole row again.  A lane has a pair first, then V experts.
 template <class T, int L, int V>
 __global__ void __launch_bounds__(kRouteThreads) zc_route_backward_kernel(RouteArgs a) {
+  after_previous();
   constexpr uint32_t kTok = kRouteThreads / L;
   __shared__ __align__(16) float s_row[kTok][L * V];
   const uint32_t lane = threadIdx.x % L;
@@ -342,11 +344,7 @@ cudaError_t route_launch(RouteArgs a, bool backward, cudaStream_t s) {
   const uint32_t lanes = a.group_size % V ? 0 : a.group_size / V;
   a.group_lanes = lanes & (lanes - 1) || a.groups > L ? 0 : lanes;
   const uint32_t grid = (a.tokens + kTok - 1) / kTok;
-  if (backward)
-    zc_route_backward_kernel<T, L, V><<<grid, kRouteThreads, 0, s>>>(a);
-  else
-    zc_route_kernel<T, L, V><<<grid, kRouteThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch(backward ? zc_route_backward_kernel<T, L, V> : zc_route_kernel<T, L, V>, grid, kRouteThreads, 0, s, a);
 }
 
 // A warp takes a token; 8 lanes do where they hold its experts, 8 each, its
@@ -428,8 +426,7 @@ __device__ __forceinline__ uint32_t plan_key(int32_t id, uint32_t experts) { ret
 
 __global__ void __launch_bounds__(kCountThreads) zc_plan_count_kernel(PlanArgs a) {
   __shared__ uint32_t h[kMaxExperts + 1];
-  // the placing kernel may start: it waits for this one where it needs the counts
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_previous();  // from here on the placing kernel may start: it waits for this one where it needs the counts
   for (uint32_t e = threadIdx.x; e <= a.experts; e += kCountThreads) h[e] = 0;
   __syncthreads();
   const uint32_t lo = blockIdx.x * kPlanGroup * a.run, hi = min(lo + kPlanGroup * a.run, a.pairs);
@@ -442,6 +439,7 @@ __global__ void __launch_bounds__(kCountThreads) zc_plan_count_kernel(PlanArgs a
 
 __global__ void __launch_bounds__(kPlaceThreads) zc_plan_place_kernel(PlanArgs a) {
   constexpr int kThreads = kPlaceThreads, kWarps = kThreads / 32;
+  if (a.blocks == 1) after_previous();
   extern __shared__ uint32_t h[];  // [kWarps][nb] counts, then places, by warp; [nb] totals, then starts; [nb] places
   const uint32_t nb = a.experts + 1;
   uint32_t *start = h + kWarps * nb, *base = start + nb;
@@ -460,7 +458,7 @@ __global__ void __launch_bounds__(kPlaceThreads) zc_plan_place_kernel(PlanArgs a
 #pragma unroll 4
     for (uint32_t i = group * kPlanGroup * a.run + threadIdx.x; i < blockIdx.x * a.run; i += kThreads)
       atomicAdd(&base[plan_key(a.ids[i], a.experts)], 1u);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();  // the counting kernel; what came before it had ended when it let this one start
     // the threads of a bucket share the groups
     const uint32_t groups = (a.blocks + kPlanGroup - 1) / kPlanGroup;
     const uint32_t wide = (nb + 31) / 32 * 32, parts = max(1u, (uint32_t)kThreads / wide), part = threadIdx.x / wide;
@@ -546,22 +544,12 @@ void plan_split(uint64_t pairs, uint32_t* blocks, uint32_t* run) {
 }
 
 cudaError_t plan_place(const PlanArgs& a, cudaStream_t s) {
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.blocks);
-  cfg.blockDim = dim3(kPlaceThreads);
-  cfg.dynamicSmemBytes = (kPlaceThreads / 32 + 2) * (a.experts + 1) * sizeof(uint32_t);  // 139 KB for 1,024 experts
-  cfg.stream = s;
-  cfg.attrs = &at;
-  cfg.numAttrs = a.blocks > 1 ? 1 : 0;
-  if (cfg.dynamicSmemBytes > 48000) {
-    const cudaError_t e = cudaFuncSetAttribute(zc_plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)cfg.dynamicSmemBytes);
+  const size_t smem = (kPlaceThreads / 32 + 2) * (a.experts + 1) * sizeof(uint32_t);  // 139 KB for 1,024 experts
+  if (smem > 48000) {
+    const cudaError_t e = cudaFuncSetAttribute(zc_plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, zc_plan_place_kernel, a);
+  return launch(zc_plan_place_kernel, a.blocks, kPlaceThreads, smem, s, a);
 }
 
 }  // namespace
@@ -625,9 +613,10 @@ zipccl_status zipccl_moe_plan(const int32_t* d_ids, uint64_t pairs, uint32_t exp
   a.experts = experts;
   plan_split(pairs, &a.blocks, &a.run);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a.blocks > 1) zc_plan_count_kernel<<<(a.blocks + kPlanGroup - 1) / kPlanGroup, kCountThreads, 0, s>>>(a);
-  const cudaError_t e = plan_place(a, s);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ZIPCCL_OK : ZIPCCL_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  if (a.blocks > 1) e = launch(zc_plan_count_kernel, (a.blocks + kPlanGroup - 1) / kPlanGroup, kCountThreads, 0, s, a);
+  if (e == cudaSuccess) e = plan_place(a, s);
+  return e == cudaSuccess ? ZIPCCL_OK : ZIPCCL_ERR_CUDA;
 }
 
 }  // extern "C"
