@@ -41,7 +41,7 @@ struct RowArgs {
 //    in registers cost warps (the same size: 73 and 124 us at best).  Here
 //    each warp keeps a ring of row pieces in shared memory, filled by
 //    asynchronous copies two stages ahead of what it sums, over all its rows
-//    in turn: 61 and 102 us, 99% of the copy rate.  For a few tokens it is
+//    in turn: 61 and 105 us, 99 and 96% of the copy rate.  For a few tokens it is
 //    0.3 us slower than the plain form by vectors, which is not kept for that.
 // Rows whose size is no multiple of 16 bytes start at any place within 16.
 // The piped form (and dispatch) then works on the vectors of the row that is
