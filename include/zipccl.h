@@ -309,7 +309,8 @@ zipccl_status zipccl_codebook_rebuild_phase(int phase, int *base_offset, uint8_t
  *   - the calls record no device status: every index read from device memory
  *     is checked against its range, and what is out of range takes no part,
  *     as each call says;
- *   - only zipccl_moe_plan needs a workspace.
+ *   - only zipccl_moe_plan needs a workspace;
+ *   - results overlap neither inputs nor each other, but for what a call names.
  * Sums, softmax statistics, weights and states are computed in 32 bits; a
  * result of a 16-bit type is rounded once, to nearest even.  No call's
  * result depends on timing: no atomics on results, sums in a fixed order.
@@ -389,7 +390,7 @@ zipccl_status zipccl_moe_plan(const int32_t *d_ids, uint64_t pairs, uint32_t exp
  * rows of dropped pairs are zeros.  d_x: [tokens][hidden] of `type`, rows
  * row_stride values apart (0: the same row for all); d_slots:
  * [tokens][top_k], top_k <= 32; d_rows: [tokens * top_k][hidden].  A slot
- * outside the rows is skipped.  d_x and d_rows must not overlap.
+ * outside the rows is skipped.
  * The backward call sums: d_grad_x[token] = sum over the token's pairs of
  * d_grad_rows[slot], dropped pairs left out.
  */

@@ -59,11 +59,12 @@ __device__ __forceinline__ uint32_t first_lane(bool x) {
   return __ffs(who) - 1;
 }
 
-// The hardware's reciprocal (1 ulp): a score is off by 2 ulp with it, and it
-// takes 4 instructions where a division takes 10.
+// The hardware's reciprocal (1 ulp) of a number that is at least 1: a score is
+// off by 2 ulp with it, and it takes one instruction where a division takes 10.
+// What is below the smallest normal float becomes 0.
 __device__ __forceinline__ float quick_rcp(float x) {
   float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float sigmoid(float l) { return quick_rcp(1.0f + expf(-l)); }
@@ -143,14 +144,17 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, float (&c)[V], f
       }
     __syncwarp();
   }
-  // a group is kept if fewer than `kept` groups come before it; equal: the lower first
+  // a group is kept if fewer than `kept` groups come before it; equal: the
+  // lower first.  The lanes of a group share the others
   const float mine = (a.top2 && lo > -INFINITY ? hi + lo : hi) + 0.0f;
   const uint32_t g = lane / stride;
   uint32_t before = 0;
-  for (uint32_t h = 0; h < a.groups; ++h) {
-    const float y = __shfl_sync(kAll, mine, h * stride, L);
-    before += y > mine || (y == mine && h < g);
+  for (uint32_t h0 = 0; h0 < a.groups; h0 += stride) {
+    const uint32_t h = h0 + lane % stride;
+    const float y = __shfl_sync(kAll, mine, min(h * stride, (uint32_t)L - 1), L);
+    before += h < a.groups && (y > mine || (y == mine && h < g));
   }
+  for (uint32_t o = 1; o < stride; o <<= 1) before += __shfl_xor_sync(kAll, before, o);
   const bool kept = g < a.groups && before < a.kept;
   if (a.group_lanes) {
 #pragma unroll
@@ -173,9 +177,9 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, float (&c)[V], f
 // place of the lowest lane is the lowest expert among equals), and what is
 // then best in that lane: no step is one lane's alone.
 // For few tokens it takes a launch (2.6 us); for many its instructions bound
-// it: of 256 experts in 8 groups, 8 chosen, a token takes 826, 29 of them for
-// each chosen expert, 158 for the sigmoids, 166 for the groups (8,192 tokens:
-// 8.5 us; 32,768: 26.8 us, 1.3 TB/s).
+// it: of 256 experts in 8 groups, 8 chosen, a token takes 747, 29 of them for
+// each chosen expert, 141 for the groups, 102 for the sigmoids (8,192 tokens:
+// 7.6 us).
 template <class T, int L, int V>
 __global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
   static_assert(V <= L, "a lane's experts are scanned by one lane each");
