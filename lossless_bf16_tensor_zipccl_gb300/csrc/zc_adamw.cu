@@ -15,7 +15,7 @@ namespace {
 
 constexpr int kStepThreads = 256;
 // Blocks an SM holds at least.  8-bit states need the warps to cover the loads
-// (109 M values: 6 blocks 267 us, 5 273, 3 283); with 32-bit states 2 to 5 are
+// (109 M values: 6 blocks 262 us, 5 264, 4 275); with 32-bit states 2 to 5 are
 // the same there (432 us) and more than 3 cost a small call 2 us.
 template <bool k8>
 constexpr int kStepBlocks = k8 ? 6 : 3;
@@ -44,12 +44,13 @@ struct StepArgs {
 };
 static_assert(sizeof(StepArgs) < 32000, "kernel parameters are limited to 32,764 bytes");
 
-// Reciprocal by the hardware's approximation (1 ulp at most, subnormals
-// kept): the quotient it enters changes the parameter far above its last bits,
-// and an IEEE division takes 10 instructions of about 50 for a value.
+// Reciprocal of a number that is not negative by the hardware's approximation
+// (1 ulp at most): the quotient it enters changes the parameter far above its
+// last bits, and an IEEE division takes 10 instructions of about 60 for a value.
+// Below the smallest normal float it is that of the smallest normal float.
 __device__ __forceinline__ float quick_rcp(float x) {
   float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(x, 0x1p-126f)));
   return y;
 }
 

@@ -210,6 +210,33 @@ def test_route_strides_streams_and_given_outputs():
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups", [(20011, 64, 2, 1), (9001, 64, 12, 4), (12345, 256, 8, 8), (3000, 384, 6, 6)])
+def test_route_many_tokens(T, E, k, groups, score):
+    """Every token's logits are the same well separated values in an order of
+    its own (0.02 apart at least: scores 4e-6 of themselves or more), against 64 bits on the GPU."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T)
+    order = torch.rand(T, E, generator=gen, device="cuda").argsort(1)
+    l = torch.linspace(-4, 4, E, device="cuda")[order]
+    kept = max(1, groups // 2)
+    w, ids = zc.moe_route(l, k, score=score, groups=groups, groups_kept=kept, scale=2.0)
+    d = l.double()
+    best = d.view(T, groups, -1).amax(-1).topk(kept, 1).indices
+    open_ = torch.zeros(T, groups, dtype=torch.bool, device="cuda").scatter(1, best, True).repeat_interleave(E // groups, 1)
+    want = torch.where(open_, d, -torch.inf).topk(k, 1).indices
+    assert torch.equal(ids.long(), want)
+    s = (d.softmax(1) if score == "softmax" else d.sigmoid()).gather(1, want)
+    s = s / s.sum(1, keepdim=True)
+    near(host(w), host(2 * s), 1e-5 * host(2 * s))
+    g = torch.randn(T, k, generator=gen, device="cuda")
+    u = s * (g.double() - (s * g.double()).sum(1, keepdim=True)) * 2
+    if score == "sigmoid":
+        u = u * (1 - d.gather(1, want).sigmoid())
+    dl = torch.zeros(T, E, dtype=torch.float64, device="cuda").scatter(1, want, u)
+    near(host(zc.moe_route_backward(g, l, ids, score=score, scale=2.0)), host(dl), 2e-5 * 2 * np.abs(host(g)).max(1, keepdims=True))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E", [5, 64, 128, 256])
 def test_route_of_one_renormalised_pair_is_exact(score, E):
     torch.manual_seed(E)
@@ -359,6 +386,37 @@ def test_combine_residual_in_place():
     y = torch.randn(30, 520, device="cuda").bfloat16()
     want = zc.moe_combine(r, ds, residual=y)
     assert torch.equal(zc.moe_combine(r, ds, residual=y, out=y), want)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,k,H", [(30000, 3, 24), (20011, 2, 300), (6000, 5, 768), (5000, 3, 1030), (4100, 2, 1536),
+                                   (3000, 7, 2055), (3001, 2, 4096), (900, 9, 3333), (40, 20, 10007)])
+def test_many_tokens(T, k, H, dtype):
+    """Several turns of every warp, and rows of one piece to many, against sums in 64 bits on the GPU."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T + H)
+    new = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(dtype)  # noqa: E731
+    ids = torch.rand(T, 3 * k, generator=gen, device="cuda").topk(k, -1).indices.int()
+    ids[torch.rand(T, k, generator=gen, device="cuda") < 0.1] = -1
+    slots = zc.moe_plan(ids, 3 * k).slots
+    gone = (slots < 0)[:, :, None]
+    at = torch.where(slots < 0, -1 - slots, slots).long()
+    assert torch.equal(at.view(-1).sort().values, torch.arange(T * k, device="cuda"))
+    x, r, res, gy = new(T, H), new(T * k, H), new(T, H), new(T, H)
+    w = torch.rand(T, k, generator=gen, device="cuda") - 0.3
+    rows = zc.moe_dispatch(x, slots)
+    assert torch.equal(rows[at.view(-1)].view(T, k, H), torch.where(gone, torch.zeros((), dtype=dtype, device="cuda"), x[:, None, :].expand(T, k, H)))
+    picked = torch.where(gone, 0.0, r[at.view(-1)].view(T, k, H).double())
+    terms = picked * w.double()[:, :, None]
+    for weights, want, size in ((w, terms.sum(1) + res.double(), terms.abs().sum(1) + res.double().abs()),
+                                (None, picked.sum(1), picked.abs().sum(1))):
+        y = zc.moe_combine(r, slots, weights, residual=res) if weights is not None else zc.moe_dispatch_backward(r, slots)
+        near_rounded(host(y), host(want), 40 * U * host(size), dtype)
+    gr, gw = zc.moe_combine_backward(gy, r, slots, w)
+    want = torch.where(gone, 0.0, w.double()[:, :, None] * gy.double()[:, None, :])
+    near_rounded(host(gr[at.view(-1)]), host(want.view(T * k, H)), 2 * U * np.abs(host(want.view(T * k, H))), dtype)
+    products = picked * gy.double()[:, None, :]
+    near(host(gw), host(products.sum(-1)), (H / 32 + 20) * U * host(products.abs().sum(-1)))
 
 
 def test_offsets_past_32_bits():
