@@ -27,6 +27,7 @@ struct RowArgs {
   uint64_t hidden;
   uint32_t tokens, top_k;
   uint64_t rows;          // tokens * top_k
+  uint32_t lead;          // dispatch of rows without a common alignment: x starts `lead` bytes after src
 };
 
 // Two forms of the kernels.
@@ -34,8 +35,8 @@ struct RowArgs {
 //    that narrow rows fill it too.  Dispatch of rows that are multiples of 16
 //    bytes takes it, a vector at a time: it only stores what it has loaded
 //    once, and stores wait for nothing (16,384 x 4,096 bf16, two pairs: 61 us,
-//    99% of the measured copy rate).  Elsewhere it goes value by value, for
-//    buffers that do not start at a multiple of 16 bytes.
+//    99% of the measured copy rate).  Elsewhere it goes value by value: where
+//    results or the experts' rows do not start at a multiple of 16 bytes.
 //  - Piped: combine and its gradient gather rows, so a warp that loads, sums
 //    and stores waits for a slot and then for a row each time, and more loads
 //    in registers cost warps (the same size: 73 and 124 us at best).  Here
@@ -284,12 +285,13 @@ struct Pipe {
 // alignment; the piece starts at byte `at` (of `total`) of the buffer, `at`
 // mod 16 into the stage.  Lane's units lane, lane + lanes, ... of
 // V * lanes + kExtra, those below `count`, exist; units outside the buffer are
-// left out and one that passes its end is cut there.
+// left out, one that passes its end is cut there, and of one that starts
+// before its first byte (`lead` after a multiple of 16) the rest is read singly.
 template <int V, int kExtra>
 __device__ __forceinline__ void copy_cover(uint32_t stage, const void* buffer, int64_t at, int64_t total, uint32_t lane,
-                                           uint32_t lanes, int32_t count) {
+                                           uint32_t lanes, int32_t count, uint32_t lead = 0) {
   const int64_t at0 = (at & ~int64_t(15)) + 16 * lane;
-  const bool inside = (at & ~int64_t(15)) >= 0 && (at & ~int64_t(15)) + 16 * (int64_t)(V * lanes + kExtra) <= total;
+  const bool inside = (at & ~int64_t(15)) >= (int64_t)lead && (at & ~int64_t(15)) + 16 * (int64_t)(V * lanes + kExtra) <= total;
   const uint8_t* from = static_cast<const uint8_t*>(buffer) + at0;
   uint32_t to = stage + 16 * lane;
 #pragma unroll
@@ -298,7 +300,13 @@ __device__ __forceinline__ void copy_cover(uint32_t stage, const void* buffer, i
     if ((int32_t)(i * lanes + lane) < count) {
       const int64_t b = at0 + 16 * (int64_t)(i * lanes);
       if (inside) copy16(to + 16 * i * lanes, from + 16 * i * lanes);
-      else if (b >= 0 && b < total) copy16(to + 16 * i * lanes, from + 16 * i * lanes, (uint32_t)min(total - b, (int64_t)16));
+      else if (b >= (int64_t)lead && b < total) copy16(to + 16 * i * lanes, from + 16 * i * lanes, (uint32_t)min(total - b, (int64_t)16));
+      else if (b == 0 && lead) {
+        for (uint32_t j = lead; j < 16 && j < total; j += 2)
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 16 * i * lanes + j),
+                       "h"(*reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(buffer) + j))
+                       : "memory");
+      }
     }
   }
 }
@@ -670,9 +678,9 @@ __global__ void __launch_bounds__(kPipeThreads) zc_dispatch_odd_kernel(RowArgs a
   auto copy = [&](uint32_t item, uint32_t stage) {
     if (item < items) {
       const uint32_t t = item / q.pieces, piece = item - t * q.pieces;
-      const int64_t first = (int64_t)piece * lanes * V, row = (int64_t)t * step;
+      const int64_t first = (int64_t)piece * lanes * V, row = (int64_t)t * step + a.lead;
       copy_cover<V, 2>(mine + stage * group_stage + 16, a.src, row + 16 * first - (first ? 15 : 0), row + (int64_t)q.bytes,
-                       lane, lanes, (int32_t)((q.bytes + 15) / 16 - first) + 2);
+                       lane, lanes, (int32_t)((q.bytes + 15) / 16 - first) + 2, a.lead);
     }
     copy_commit();
   };
@@ -684,7 +692,7 @@ __global__ void __launch_bounds__(kPipeThreads) zc_dispatch_odd_kernel(RowArgs a
     __syncwarp();
     if (item < items) {
       const uint32_t t = item / q.pieces, piece = item - t * q.pieces;
-      const int64_t first = (int64_t)piece * lanes * V, row_at = (int64_t)t * step;
+      const int64_t first = (int64_t)piece * lanes * V, row_at = (int64_t)t * step + a.lead;
       const int64_t kept0 = ((row_at + 16 * first - (first ? 15 : 0)) & ~int64_t(15)) - row_at;
       const uint32_t from = mine + (turn & 1) * group_stage + 16;
       for (uint32_t k = 0; k < a.top_k; ++k) {
@@ -794,16 +802,19 @@ cudaError_t pipe_by_width(RowOp op, const RowArgs& a, cudaStream_t s) {
 }
 
 template <class T>
-cudaError_t row_form(RowOp op, const RowArgs& a, cudaStream_t s) {
+cudaError_t row_form(RowOp op, RowArgs& a, cudaStream_t s) {
   constexpr uint32_t z = sizeof(T), N = 16 / z;
-  // the piped form starts at multiples of 16 bytes and counts pieces in 32 bits
-  const bool base = host_aligned(a.src, 16) && host_aligned(a.side, 16) && host_aligned(a.dst, 16) && a.hidden &&
-                    a.hidden * z < (1ull << 30) && (uint64_t)a.tokens * ((a.hidden + 511) / 512 + 1) < (1ull << 31);
-  const bool even = a.hidden % N == 0 && (op != RowOp::kDispatch || a.stride % N == 0);
-  if (!base) return plain_launch<T, 1>(op, a, s);
-  if (!even) return pipe_by_width<T, true>(op, a, s);
-  if (op == RowOp::kDispatch) return plain_launch<T, N>(op, a, s);
-  return pipe_by_width<T, false>(op, a, s);
+  // pieces are counted in 32 bits; buffers start at multiples of 16 bytes, but
+  // for the x of dispatch
+  const bool pipe = host_aligned(a.side, 16) && host_aligned(a.dst, 16) && a.hidden && a.hidden * z < (1ull << 30) &&
+                    (uint64_t)a.tokens * ((a.hidden + 511) / 512 + 1) < (1ull << 31) &&
+                    (op == RowOp::kDispatch || host_aligned(a.src, 16));
+  if (!pipe) return plain_launch<T, 1>(op, a, s);
+  if (op != RowOp::kDispatch) return a.hidden % N ? pipe_by_width<T, true>(op, a, s) : pipe_by_width<T, false>(op, a, s);
+  if (host_aligned(a.src, 16) && a.hidden % N == 0 && a.stride % N == 0) return plain_launch<T, N>(op, a, s);
+  a.lead = (uint32_t)(reinterpret_cast<uintptr_t>(a.src) & 15);
+  a.src = static_cast<const uint8_t*>(a.src) - a.lead;
+  return pipe_by_width<T, true>(op, a, s);
 }
 
 zipccl_status rows(RowOp op, RowArgs& a, int type, uint64_t tokens, uint32_t top_k, uint64_t hidden, void* stream) {
