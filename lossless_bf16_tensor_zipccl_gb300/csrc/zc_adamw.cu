@@ -122,16 +122,22 @@ __device__ __forceinline__ void store1(T* p, float x) { *p = from_float<T>(x); }
 // ends within the 256, 32 apart for eight narrow ones.
 template <bool kWide, class T>
 __device__ __forceinline__ void load(const T* p, uint32_t lane, uint32_t left, float (&x)[8]) {
-  if (kWide) return load8(p + 8 * lane, x);
+  if constexpr (kWide) {
+    load8(p + 8 * lane, x);
+  } else {
 #pragma unroll
-  for (uint32_t j = 0; j < 8; ++j) x[j] = 32 * j + lane < left ? load1(p + 32 * j + lane) : 0.0f;
+    for (uint32_t j = 0; j < 8; ++j) x[j] = 32 * j + lane < left ? load1(p + 32 * j + lane) : 0.0f;
+  }
 }
 template <bool kWide, class T>
 __device__ __forceinline__ void store(T* p, uint32_t lane, uint32_t left, const float (&x)[8]) {
-  if (kWide) return store8(p + 8 * lane, x);
+  if constexpr (kWide) {
+    store8(p + 8 * lane, x);
+  } else {
 #pragma unroll
-  for (uint32_t j = 0; j < 8; ++j)
-    if (32 * j + lane < left) store1(p + 32 * j + lane, x[j]);
+    for (uint32_t j = 0; j < 8; ++j)
+      if (32 * j + lane < left) store1(p + 32 * j + lane, x[j]);
+  }
 }
 
 __device__ __forceinline__ float max_nan(float x, float y) {
