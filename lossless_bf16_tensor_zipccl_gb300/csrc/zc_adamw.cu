@@ -44,13 +44,20 @@ struct StepArgs {
 };
 static_assert(sizeof(StepArgs) < 32000, "kernel parameters are limited to 32,764 bytes");
 
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+
 // Reciprocal of a number that is not negative by the hardware's approximation
 // (1 ulp at most): the quotient it enters changes the parameter far above its
 // last bits, and an IEEE division takes 10 instructions of about 60 for a value.
-// Below the smallest normal float it is that of the smallest normal float.
+// Below the smallest normal float it is that of the smallest normal float; of
+// NaN (a second moment that is not a number) it is NaN.
 __device__ __forceinline__ float quick_rcp(float x) {
   float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(x, 0x1p-126f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(max_nan(x, 0x1p-126f)));
   return y;
 }
 
@@ -138,12 +145,6 @@ __device__ __forceinline__ void store(T* p, uint32_t lane, uint32_t left, const 
     for (uint32_t j = 0; j < 8; ++j)
       if (32 * j + lane < left) store1(p + 32 * j + lane, x[j]);
   }
-}
-
-__device__ __forceinline__ float max_nan(float x, float y) {
-  float z;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
-  return z;
 }
 
 // Scales a block of 256 values held by a warp, 8 a lane, to E4M3's range: the

@@ -1,0 +1,65 @@
+"""The operators around the exchange on the GPU: values, streams, threads and
+kinds of arguments beside those of test_operators_gpu.  Tolerances are derived
+at each test; u = 2^-24 is half a unit in the last place of a float."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import lossless_bf16_tensor_zipccl_gb300 as zc  # noqa: E402
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    zc.load()
+    yield
+
+
+# ------------------------------------------------------------------ AdamW, what is not finite
+@pytest.mark.parametrize("ptype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("first", [0, 1])
+def test_adamw_8_bit_root_that_overflowed_makes_its_parameter_nan(ptype, first):
+    """A finite gradient whose square is infinite: the first step divides by
+    infinity, the second moment's code is then NaN and the first one's is not,
+    and the next step's parameter is NaN there and nowhere else."""
+    n = 256 * 3 + 40
+    at = torch.tensor([3, 300, n - 1], device="cuda")
+    flat = lambda dtype: torch.zeros(n + 8, dtype=dtype, device="cuda")[first:first + n]  # noqa: E731
+    p, g = flat(ptype), flat(torch.float32)
+    p += 0.5
+    g += 1e-3
+    g[at] = torch.tensor([1e20, -3e19, 1e20], device="cuda")
+    m, v, ms, vs = zc.adamw_state(p, bits=8)
+    how = dict(scales=([ms], [vs]), lr=3e-4, betas=(0.9, 0.95), weight_decay=0.0)
+    zc.adamw_step([p], [g], [m], [v], step=1, **how)
+    odd = torch.zeros(n, dtype=torch.bool, device="cuda")
+    odd[at] = True
+    assert torch.isfinite(p).all() and (p[odd] == 0.5).all()
+    assert torch.isfinite(m.float()).all() and torch.equal(torch.isnan(v.float()), odd)
+    g.zero_()
+    zc.adamw_step([p], [g], [m], [v], step=2, **how)
+    assert torch.equal(torch.isnan(p), odd) and torch.isfinite(p[~odd]).all()
+
+
+@pytest.mark.parametrize("ptype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("first", [0, 1])
+def test_adamw_32_bit_second_moment_that_is_not_a_number(ptype, first):
+    """NaN, or negative and so without a root, as a damaged checkpoint has them;
+    an infinite one divides: no change but the decay."""
+    n = 256 + 30
+    flat = lambda dtype, x: torch.full((n + 8,), x, dtype=dtype, device="cuda")[first:first + n]  # noqa: E731
+    p, g, m, v = flat(ptype, 0.5), flat(torch.float32, 1e-3), flat(torch.float32, 1e-3), flat(torch.float32, 1e-6)
+    v[5], v[n - 1], v[17] = float("nan"), -1.0, float("inf")
+    m[6] = 0.0
+    v[6] = float("nan")
+    odd = torch.zeros(n, dtype=torch.bool, device="cuda")
+    odd[[5, 6, n - 1]] = True
+    zc.adamw_step([p], [g], [m], [v], step=4, lr=3e-4, weight_decay=0.0)
+    assert torch.equal(torch.isnan(p), odd) and torch.isfinite(p[~odd]).all() and p[17].item() == 0.5
+    assert (p[~odd][:5] < 0.5).all() if ptype == torch.float32 else True
