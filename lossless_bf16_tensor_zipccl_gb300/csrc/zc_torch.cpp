@@ -13,6 +13,7 @@
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -47,16 +48,24 @@ int value_type(const Tensor& t, const char* what) {
   }
 }
 
-// A contiguous CUDA tensor of this type and shape.
-const Tensor& plain(const Tensor& t, ScalarType type, IntArrayRef shape, const char* what) {
+// The device of a call's tensors: that of the first of them.
+c10::Device cuda_device(const Tensor& t, const char* what) {
+  if (!t.is_cuda()) refuse(PyExc_ValueError, "%s: expected a CUDA tensor", what);
+  return t.device();
+}
+
+// A contiguous tensor of this type and shape on this device: the kernels read
+// every operand of a call through plain pointers.
+const Tensor& plain(const Tensor& t, ScalarType type, IntArrayRef shape, c10::Device device, const char* what) {
   if (t.scalar_type() != type) refuse(PyExc_TypeError, "%s: expected %s, got %s", what, toString(type), toString(t.scalar_type()));
   if (t.sizes() != shape) refuse(PyExc_ValueError, "%s: a tensor of another shape was expected", what);
   if (!t.is_cuda() || !t.is_contiguous()) refuse(PyExc_ValueError, "%s: expected a contiguous CUDA tensor", what);
+  if (t.device() != device) refuse(PyExc_ValueError, "%s: expected a tensor on the device of the call's others", what);
   return t;
 }
 
-const void* optional(PyObject* o, ScalarType type, IntArrayRef shape, const char* what) {
-  return o == Py_None ? nullptr : plain(tensor(o, what), type, shape, what).const_data_ptr();
+const void* optional(PyObject* o, ScalarType type, IntArrayRef shape, c10::Device device, const char* what) {
+  return o == Py_None ? nullptr : plain(tensor(o, what), type, shape, device, what).const_data_ptr();
 }
 
 void two_dims(const Tensor& t, const char* what) {
@@ -83,15 +92,16 @@ double real(PyObject* o) {
   return v;
 }
 
-// The stream of a call (None: the current one of the tensors' device) and the
-// results it allocates: memory that another stream works on must not be handed
-// out again before that work is done.
+// A call's device, current until the call ends: the launches go to the current
+// device, and stream 0 is that device's.  Its stream (None: the current one of
+// that device) and the results it allocates: memory that another stream works
+// on must not be handed out again before that work is done.
 struct Call {
   c10::Device device;
+  c10::cuda::CUDAGuard current_device;
   cudaStream_t stream;
   bool other = false;
-  Call(const Tensor& like, PyObject* s) : device(like.device()) {
-    if (!like.is_cuda()) refuse(PyExc_ValueError, "expected CUDA tensors");
+  Call(c10::Device d, PyObject* s) : device(d), current_device(d) {
     const cudaStream_t current = c10::cuda::getCurrentCUDAStream(device.index()).stream();
     stream = current;
     if (s != Py_None) {
@@ -107,7 +117,7 @@ struct Call {
     return t;
   }
   Tensor result(PyObject* o, IntArrayRef shape, ScalarType type, const char* what) const {
-    return o == Py_None ? empty(shape, type) : plain(tensor(o, what), type, shape, what);
+    return o == Py_None ? empty(shape, type) : plain(tensor(o, what), type, shape, device, what);
   }
 };
 
@@ -149,13 +159,14 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int type = value_type(logits, "logits");
   const uint64_t stride = row_stride(logits, "logits");
   const int64_t tokens = logits.size(0), experts = logits.size(1), k = o.top_k;
-  const void* bias = optional(a[8], ScalarType::Float, {experts}, "bias");
+  const c10::Device device = logits.device();
+  const void* bias = optional(a[8], ScalarType::Float, {experts}, device, "bias");
   const void* mask = nullptr;
   if (a[9] != Py_None) {
     const Tensor& m = tensor(a[9], "mask");
-    mask = plain(m, m.scalar_type() == ScalarType::Byte ? ScalarType::Byte : ScalarType::Bool, {tokens}, "mask").const_data_ptr();
+    mask = plain(m, m.scalar_type() == ScalarType::Byte ? ScalarType::Byte : ScalarType::Bool, {tokens}, device, "mask").const_data_ptr();
   }
-  const Call call(logits, a[12]);
+  const Call call(device, a[12]);
   const Tensor weights = call.result(a[10], {tokens, k}, ScalarType::Float, "weights");
   const Tensor ids = call.result(a[11], {tokens, k}, ScalarType::Int, "ids");
   return answer(zipccl_moe_route(logits.const_data_ptr(), type, stride, tokens, experts, &o, static_cast<const float*>(bias),
@@ -175,15 +186,16 @@ PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& ids = tensor(a[2], "ids");
   two_dims(ids, "ids");
   const int64_t tokens = logits.size(0), experts = logits.size(1), k = ids.size(1);
-  plain(ids, ScalarType::Int, {tokens, k}, "ids");
-  const Tensor& grad = plain(tensor(a[0], "grad_weights"), ScalarType::Float, {tokens, k}, "grad_weights");
+  const c10::Device device = logits.device();
+  plain(ids, ScalarType::Int, {tokens, k}, device, "ids");
+  const Tensor& grad = plain(tensor(a[0], "grad_weights"), ScalarType::Float, {tokens, k}, device, "grad_weights");
   zipccl_route_options o{};
   o.top_k = (uint32_t)k;
   o.score = (int32_t)integer(a[3]);
   o.renormalize = (int32_t)integer(a[4]);
   o.scale = (float)real(a[5]);
   o.groups = o.groups_kept = 1;
-  const Call call(logits, a[7]);
+  const Call call(device, a[7]);
   const Tensor out = call.result(a[6], {tokens, experts}, logits.scalar_type(), "grad_logits");
   return answer(zipccl_moe_route_backward(static_cast<const float*>(grad.const_data_ptr()), logits.const_data_ptr(), type,
                                           stride, tokens, experts, &o, static_cast<const int32_t*>(ids.const_data_ptr()),
@@ -198,12 +210,12 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   count(n, 7);
   const Tensor& ids = tensor(a[0], "ids");
   const int64_t experts = integer(a[1]);
-  plain(ids, ScalarType::Int, ids.sizes(), "ids");
+  plain(ids, ScalarType::Int, ids.sizes(), ids.device(), "ids");
   uint64_t need = 0;
   if (experts < 1 || experts > UINT32_MAX) refuse(PyExc_ValueError, "n_experts is at least 1");
   const zipccl_status st = zipccl_moe_plan_workspace_bytes(ids.numel(), (uint32_t)experts, &need);
   if (st != ZIPCCL_OK) return PyLong_FromLong(st);
-  const Call call(ids, a[6]);
+  const Call call(ids.device(), a[6]);
   const Tensor counts = call.result(a[2], {experts}, ScalarType::Int, "counts");
   const Tensor offsets = call.result(a[3], {experts + 1}, ScalarType::Int, "offsets");
   const Tensor slots = call.result(a[4], ids.sizes(), ScalarType::Int, "slots");
@@ -211,7 +223,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (need) {
     if (a[5] != Py_None) ws = tensor(a[5], "ws");
     if (!ws.defined() || ws.nbytes() < need) ws = call.empty({(int64_t)need}, ScalarType::Byte);
-    if (!ws.is_cuda() || !ws.is_contiguous()) refuse(PyExc_ValueError, "ws: expected a contiguous CUDA tensor");
+    plain(ws, ws.scalar_type(), ws.sizes(), call.device, "ws");
   }
   return answer(zipccl_moe_plan(static_cast<const int32_t*>(ids.const_data_ptr()), ids.numel(), (uint32_t)experts,
                                 static_cast<int32_t*>(counts.data_ptr()), static_cast<int32_t*>(offsets.data_ptr()),
@@ -221,9 +233,9 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-const int32_t* pair_slots(const Tensor& slots, int64_t tokens) {
+const int32_t* pair_slots(const Tensor& slots, int64_t tokens, c10::Device device) {
   two_dims(slots, "slots");
-  return static_cast<const int32_t*>(plain(slots, ScalarType::Int, {tokens, slots.size(1)}, "slots").const_data_ptr());
+  return static_cast<const int32_t*>(plain(slots, ScalarType::Int, {tokens, slots.size(1)}, device, "slots").const_data_ptr());
 }
 
 // x, slots, out, stream
@@ -234,8 +246,8 @@ PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int type = value_type(x, "x");
   const uint64_t stride = row_stride(x, "x");
   const int64_t tokens = x.size(0), hidden = x.size(1);
-  const int32_t* at = pair_slots(slots, tokens);
-  const Call call(x, a[3]);
+  const int32_t* at = pair_slots(slots, tokens, x.device());
+  const Call call(x.device(), a[3]);
   const Tensor out = call.result(a[2], {tokens * slots.size(1), hidden}, x.scalar_type(), "out");
   return answer(zipccl_moe_dispatch(x.const_data_ptr(), type, stride, tokens, (uint32_t)slots.size(1), hidden, at,
                                     out.data_ptr(), call.stream),
@@ -254,10 +266,10 @@ struct Pairs {
     two_dims(slots, "slots");
     tokens = slots.size(0);
     k = slots.size(1);
-    at = pair_slots(slots, tokens);
+    at = pair_slots(slots, tokens, cuda_device(rows, what));
     two_dims(rows, what);
     hidden = rows.size(1);
-    plain(rows, rows.scalar_type(), {tokens * k, hidden}, what);
+    plain(rows, rows.scalar_type(), {tokens * k, hidden}, rows.device(), what);
   }
 };
 
@@ -266,7 +278,7 @@ PyObject* dispatch_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 4);
   const Pairs p(a[0], a[1], "grad_rows");
-  const Call call(p.rows, a[3]);
+  const Call call(p.rows.device(), a[3]);
   const Tensor out = call.result(a[2], {p.tokens, p.hidden}, p.rows.scalar_type(), "out");
   return answer(zipccl_moe_dispatch_backward(p.rows.const_data_ptr(), p.type, p.tokens, (uint32_t)p.k, p.hidden, p.at,
                                              out.data_ptr(), call.stream),
@@ -279,9 +291,10 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 6);
   const Pairs p(a[0], a[1], "rows");
-  const void* weights = optional(a[2], ScalarType::Float, {p.tokens, p.k}, "weights");
-  const void* residual = optional(a[3], p.rows.scalar_type(), {p.tokens, p.hidden}, "residual");
-  const Call call(p.rows, a[5]);
+  const c10::Device device = p.rows.device();
+  const void* weights = optional(a[2], ScalarType::Float, {p.tokens, p.k}, device, "weights");
+  const void* residual = optional(a[3], p.rows.scalar_type(), {p.tokens, p.hidden}, device, "residual");
+  const Call call(device, a[5]);
   const Tensor out = call.result(a[4], {p.tokens, p.hidden}, p.rows.scalar_type(), "out");
   return answer(zipccl_moe_combine(p.rows.const_data_ptr(), p.type, p.tokens, (uint32_t)p.k, p.hidden, p.at,
                                    static_cast<const float*>(weights), residual, out.data_ptr(), call.stream),
@@ -295,9 +308,10 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   count(n, 7);
   const Pairs p(a[1], a[2], "rows");
   const ScalarType type = p.rows.scalar_type();
-  const Tensor& grad = plain(tensor(a[0], "grad_out"), type, {p.tokens, p.hidden}, "grad_out");
-  const void* weights = optional(a[3], ScalarType::Float, {p.tokens, p.k}, "weights");
-  const Call call(p.rows, a[6]);
+  const c10::Device device = p.rows.device();
+  const Tensor& grad = plain(tensor(a[0], "grad_out"), type, {p.tokens, p.hidden}, device, "grad_out");
+  const void* weights = optional(a[3], ScalarType::Float, {p.tokens, p.k}, device, "weights");
+  const Call call(device, a[6]);
   const Tensor grad_rows = call.result(a[4], p.rows.sizes(), type, "grad_rows");
   const Tensor grad_weights = call.result(a[5], {p.tokens, p.k}, ScalarType::Float, "grad_weights");
   return answer(zipccl_moe_combine_backward(grad.const_data_ptr(), p.rows.const_data_ptr(), p.type, p.tokens, (uint32_t)p.k,
@@ -320,8 +334,8 @@ struct Sequence {
 };
 
 // The addresses of one list of tensors, into one field of the records.
-void column(PyObject* list, std::vector<zipccl_adamw_tensor>& records, bool scales, ScalarType type, const char* what,
-            void (*set)(zipccl_adamw_tensor&, void*)) {
+void column(PyObject* list, std::vector<zipccl_adamw_tensor>& records, bool scales, ScalarType type, c10::Device device,
+            const char* what, void (*set)(zipccl_adamw_tensor&, void*)) {
   const Sequence s(list, what);
   if (s.n != (Py_ssize_t)records.size())
     refuse(PyExc_ValueError, "%s: expected %zd tensors, got %zd", what, (Py_ssize_t)records.size(), s.n);
@@ -330,6 +344,7 @@ void column(PyObject* list, std::vector<zipccl_adamw_tensor>& records, bool scal
     const uint64_t want = scales ? (records[i].n + ZIPCCL_ADAMW_BLOCK - 1) / ZIPCCL_ADAMW_BLOCK : records[i].n;
     if (t.scalar_type() != type) refuse(PyExc_TypeError, "%s: expected %s, got %s", what, toString(type), toString(t.scalar_type()));
     if (!t.is_cuda() || !t.is_contiguous()) refuse(PyExc_ValueError, "%s: expected contiguous CUDA tensors", what);
+    if (t.device() != device) refuse(PyExc_ValueError, "%s: expected tensors on the device of the first parameter", what);
     if ((uint64_t)t.numel() != want) refuse(PyExc_ValueError, "%s: a tensor of another size was expected", what);
     set(records[i], t.data_ptr());
   }
@@ -342,7 +357,7 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
   count(n, 15);
   std::vector<zipccl_adamw_tensor> records;
   ScalarType ptype, gtype;
-  std::optional<Call> call;
+  std::optional<c10::Device> first;
   {
     const Sequence p(a[0], "params"), g(a[1], "grads");
     if (p.n == 0) Py_RETURN_NONE;
@@ -353,33 +368,35 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (ScalarType t : {ptype, gtype})
       if (t != ScalarType::Float && t != ScalarType::BFloat16)
         refuse(PyExc_TypeError, "params and grads: expected float32 or bfloat16, got %s", toString(t));
-    call.emplace(p0, a[14]);
+    first = cuda_device(p0, "params");
     records.resize(p.n);
     for (Py_ssize_t i = 0; i < p.n; ++i) records[i] = {}, records[i].n = (uint64_t)p.at(i, "params").numel();
   }
+  const c10::Device device = *first;
   const bool small = a[4] != Py_None;
   const ScalarType state = small ? ScalarType::Float8_e4m3fn : ScalarType::Float;
-  column(a[0], records, false, ptype, "params", [](zipccl_adamw_tensor& r, void* p) { r.d_param = p; });
-  column(a[1], records, false, gtype, "grads", [](zipccl_adamw_tensor& r, void* p) { r.d_grad = p; });
-  column(a[2], records, false, state, "exp_avgs", [](zipccl_adamw_tensor& r, void* p) { r.d_exp_avg = p; });
-  column(a[3], records, false, state, "exp_avg_sqs", [](zipccl_adamw_tensor& r, void* p) { r.d_exp_avg_sq = p; });
+  column(a[0], records, false, ptype, device, "params", [](zipccl_adamw_tensor& r, void* p) { r.d_param = p; });
+  column(a[1], records, false, gtype, device, "grads", [](zipccl_adamw_tensor& r, void* p) { r.d_grad = p; });
+  column(a[2], records, false, state, device, "exp_avgs", [](zipccl_adamw_tensor& r, void* p) { r.d_exp_avg = p; });
+  column(a[3], records, false, state, device, "exp_avg_sqs", [](zipccl_adamw_tensor& r, void* p) { r.d_exp_avg_sq = p; });
   if (small) {
-    column(a[4], records, true, ScalarType::Float, "scales", [](zipccl_adamw_tensor& r, void* p) { r.d_avg_scale = (float*)p; });
-    column(a[5], records, true, ScalarType::Float, "scales", [](zipccl_adamw_tensor& r, void* p) { r.d_sq_scale = (float*)p; });
+    column(a[4], records, true, ScalarType::Float, device, "scales", [](zipccl_adamw_tensor& r, void* p) { r.d_avg_scale = (float*)p; });
+    column(a[5], records, true, ScalarType::Float, device, "scales", [](zipccl_adamw_tensor& r, void* p) { r.d_sq_scale = (float*)p; });
   }
   if (a[6] != Py_None)
-    column(a[6], records, false, ScalarType::BFloat16, "copies", [](zipccl_adamw_tensor& r, void* p) { r.d_copy = p; });
+    column(a[6], records, false, ScalarType::BFloat16, device, "copies", [](zipccl_adamw_tensor& r, void* p) { r.d_copy = p; });
   const float* scale = nullptr;
   if (a[7] != Py_None) {
     const Tensor& t = tensor(a[7], "grad_scale");
     if (t.numel() != 1) refuse(PyExc_ValueError, "grad_scale: expected one value");
-    scale = static_cast<const float*>(plain(t, ScalarType::Float, t.sizes(), "grad_scale").const_data_ptr());
+    scale = static_cast<const float*>(plain(t, ScalarType::Float, t.sizes(), device, "grad_scale").const_data_ptr());
   }
   const int64_t step = integer(a[13]);
   const zipccl_adamw_options o = {real(a[8]), real(a[9]), real(a[10]), real(a[11]), real(a[12]), (uint64_t)std::max<int64_t>(step, 0)};
+  const Call call(device, a[14]);
   const zipccl_status st =
       zipccl_adamw_step(records.data(), (uint32_t)records.size(), ptype == ScalarType::Float ? ZIPCCL_TYPE_F32 : ZIPCCL_TYPE_BF16,
-                        gtype == ScalarType::Float ? ZIPCCL_TYPE_F32 : ZIPCCL_TYPE_BF16, small ? 8 : 32, &o, scale, call->stream);
+                        gtype == ScalarType::Float ? ZIPCCL_TYPE_F32 : ZIPCCL_TYPE_BF16, small ? 8 : 32, &o, scale, call.stream);
   if (st != ZIPCCL_OK) return PyLong_FromLong(st);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS

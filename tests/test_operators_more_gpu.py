@@ -63,3 +63,37 @@ def test_adamw_32_bit_second_moment_that_is_not_a_number(ptype, first):
     zc.adamw_step([p], [g], [m], [v], step=4, lr=3e-4, weight_decay=0.0)
     assert torch.equal(torch.isnan(p), odd) and torch.isfinite(p[~odd]).all() and p[17].item() == 0.5
     assert (p[~odd][:5] < 0.5).all() if ptype == torch.float32 else True
+
+
+# ------------------------------------------------------------------ devices and streams
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on a second GPU, and has no memory."""
+    @staticmethod
+    def __new__(cls, *shape, dtype):
+        return torch.Tensor._make_wrapper_subclass(cls, shape, dtype=dtype, device="cuda:1")
+
+    @classmethod
+    def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+        raise AssertionError(f"{func} on a tensor without memory")
+
+
+def test_given_results_on_another_device_are_refused():
+    f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+    l, g = torch.zeros(4, 8, device="cuda"), torch.zeros(4, 2, device="cuda")
+    ids, r = torch.zeros(4, 2, dtype=i32, device="cuda"), torch.zeros(8, 8, device="cuda")
+    many = torch.zeros(1 << 16, dtype=i32, device="cuda")
+    need = zc.zipccl_moe_plan_workspace_bytes(1 << 16, 8)
+    for call in (lambda: zc.moe_route(l, 2, weights=Elsewhere(4, 2, dtype=f32)),
+                 lambda: zc.moe_route(l, 2, ids=Elsewhere(4, 2, dtype=i32)),
+                 lambda: zc.moe_route_backward(g, l, ids, grad_logits=Elsewhere(4, 8, dtype=f32)),
+                 lambda: zc.moe_plan(ids, 8, counts=Elsewhere(8, dtype=i32)),
+                 lambda: zc.moe_plan(ids, 8, offsets=Elsewhere(9, dtype=i32)),
+                 lambda: zc.moe_plan(ids, 8, slots=Elsewhere(4, 2, dtype=i32)),
+                 lambda: zc.moe_plan(many, 8, ws=Elsewhere(need, dtype=u8)),
+                 lambda: zc.moe_dispatch(l, ids, out=Elsewhere(8, 8, dtype=f32)),
+                 lambda: zc.moe_dispatch_backward(r, ids, out=Elsewhere(4, 8, dtype=f32)),
+                 lambda: zc.moe_combine(r, ids, out=Elsewhere(4, 8, dtype=f32)),
+                 lambda: zc.moe_combine_backward(l, r, ids, grad_rows=Elsewhere(8, 8, dtype=f32)),
+                 lambda: zc.moe_combine_backward(l, r, ids, grad_weights=Elsewhere(4, 2, dtype=f32))):
+        with pytest.raises(ValueError):
+            call()
