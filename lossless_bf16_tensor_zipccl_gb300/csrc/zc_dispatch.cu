@@ -13,7 +13,6 @@ namespace {
 
 constexpr uint32_t kMaxTopK = 32;
 constexpr int kRowThreads = 256;
-constexpr int kMaxDevices = 64;
 constexpr uint32_t kPipeSmemMax = 110 << 10;
 
 struct RowArgs {

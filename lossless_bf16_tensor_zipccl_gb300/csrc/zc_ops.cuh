@@ -12,6 +12,7 @@
 namespace zc {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kMaxDevices = 64;  // devices of a process that what is looked up once is kept for
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }

@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "zc_ops.cuh"
 #include "zipccl.h"
 
@@ -547,13 +549,21 @@ void plan_split(uint64_t pairs, uint32_t* blocks, uint32_t* run) {
   *blocks = pairs ? (uint32_t)((pairs + r - 1) / r) : 1;
 }
 
-cudaError_t plan_place(const PlanArgs& a, cudaStream_t s) {
-  const size_t smem = (kPlaceThreads / 32 + 2) * (a.experts + 1) * sizeof(uint32_t);  // 139 KB for 1,024 experts
-  if (smem > 48000) {
-    const cudaError_t e = cudaFuncSetAttribute(zc_plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  return launch(zc_plan_place_kernel, a.blocks, kPlaceThreads, smem, s, a);
+size_t plan_smem(uint32_t experts) { return (kPlaceThreads / 32 + 2) * (experts + 1) * sizeof(uint32_t); }
+
+// Allows the placing kernel the 139 KB that 1,024 experts take, once for each
+// device: the limit is the kernel's, shared by every thread's calls, so no call
+// sets it to its own need, nor finds it below that.
+cudaError_t plan_allow_smem() {
+  static std::atomic<bool> allowed[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (allowed[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(zc_plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem(kMaxExperts));
+  if (e == cudaSuccess) allowed[dev].store(true, std::memory_order_release);
+  return e;
 }
 
 }  // namespace
@@ -617,9 +627,11 @@ zipccl_status zipccl_moe_plan(const int32_t* d_ids, uint64_t pairs, uint32_t exp
   a.experts = experts;
   plan_split(pairs, &a.blocks, &a.run);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaSuccess;
-  if (a.blocks > 1) e = launch(zc_plan_count_kernel, (a.blocks + kPlanGroup - 1) / kPlanGroup, kCountThreads, 0, s, a);
-  if (e == cudaSuccess) e = plan_place(a, s);
+  const size_t smem = plan_smem(experts);
+  cudaError_t e = smem > 48000 ? plan_allow_smem() : cudaSuccess;
+  if (e == cudaSuccess && a.blocks > 1)
+    e = launch(zc_plan_count_kernel, (a.blocks + kPlanGroup - 1) / kPlanGroup, kCountThreads, 0, s, a);
+  if (e == cudaSuccess) e = launch(zc_plan_place_kernel, a.blocks, kPlaceThreads, smem, s, a);
   return e == cudaSuccess ? ZIPCCL_OK : ZIPCCL_ERR_CUDA;
 }
 

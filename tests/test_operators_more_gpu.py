@@ -3,6 +3,8 @@ kinds of arguments beside those of test_operators_gpu.  Tolerances are derived
 at each test; u = 2^-24 is half a unit in the last place of a float."""
 from __future__ import annotations
 
+import threading
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -97,3 +99,34 @@ def test_given_results_on_another_device_are_refused():
                  lambda: zc.moe_combine_backward(l, r, ids, grad_weights=Elsewhere(4, 2, dtype=f32))):
         with pytest.raises(ValueError):
             call()
+
+
+# ------------------------------------------------------------------ host threads
+def test_plans_of_two_threads_with_different_expert_counts():
+    """400 experts (54 KB of shared memory) and 1,024 (139 KB) at once, through
+    the calls that leave Python's lock: every call succeeds and has its answer."""
+    def work(experts, turns, out):
+        torch.cuda.set_device(0)
+        gen = torch.Generator().manual_seed(experts)
+        ids = torch.randint(-1, experts, (1500,), generator=gen, dtype=torch.int32).cuda()
+        counts, offsets, slots = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (experts, experts + 1, 1500))
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        at = [t.data_ptr() for t in (ids, counts, offsets, slots)]
+        bad = 0
+        for _ in range(turns):
+            bad += zc.zipccl_moe_plan(at[0], 1500, experts, *at[1:], 0, 0, stream.cuda_stream) != zc.OK
+        stream.synchronize()
+        want = torch.bincount(ids[ids >= 0].long(), minlength=experts)
+        key = torch.where(ids < 0, experts, ids)
+        row = torch.empty_like(ids)
+        row[key.sort(stable=True).indices] = torch.arange(1500, dtype=torch.int32, device="cuda")
+        out.append((experts, bad, torch.equal(counts.long(), want), torch.equal(slots, torch.where(ids < 0, -1 - row, row))))
+
+    out = []
+    threads = [threading.Thread(target=work, args=(e, 4000, out)) for e in (400, 1024, 400, 1024)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert sorted(out) == [(400, 0, True, True)] * 2 + [(1024, 0, True, True)] * 2
