@@ -94,8 +94,10 @@ double real(PyObject* o) {
 
 // A call's device, current until the call ends: the launches go to the current
 // device, and stream 0 is that device's.  Its stream (None: the current one of
-// that device) and the results it allocates: memory that another stream works
-// on must not be handed out again before that work is done.
+// that device) and the results it allocates.  They come from the memory of the
+// stream that writes them: what the current stream has freed it may still be
+// reading.  A result is the current stream's to read, so its memory goes back
+// only after what that stream has queued when it is freed.
 struct Call {
   c10::Device device;
   c10::cuda::CUDAGuard current_device;
@@ -110,10 +112,15 @@ struct Call {
       other = stream != current;
     }
   }
+  Tensor scratch(IntArrayRef shape, ScalarType type) const {
+    if (!other) return at::detail::empty_cuda(shape, type, device, std::nullopt);
+    const c10::cuda::CUDAStreamGuard its(c10::cuda::getStreamFromExternal(stream, device.index()));
+    return at::detail::empty_cuda(shape, type, device, std::nullopt);
+  }
   Tensor empty(IntArrayRef shape, ScalarType type) const {
-    Tensor t = at::detail::empty_cuda(shape, type, device, std::nullopt);
+    Tensor t = scratch(shape, type);
     if (other)
-      c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), c10::cuda::getStreamFromExternal(stream, device.index()));
+      c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), c10::cuda::getCurrentCUDAStream(device.index()));
     return t;
   }
   Tensor result(PyObject* o, IntArrayRef shape, ScalarType type, const char* what) const {
@@ -222,7 +229,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor ws;
   if (need) {
     if (a[5] != Py_None) ws = tensor(a[5], "ws");
-    if (!ws.defined() || ws.nbytes() < need) ws = call.empty({(int64_t)need}, ScalarType::Byte);
+    if (!ws.defined() || ws.nbytes() < need) ws = call.scratch({(int64_t)need}, ScalarType::Byte);
     plain(ws, ws.scalar_type(), ws.sizes(), call.device, "ws");
   }
   return answer(zipccl_moe_plan(static_cast<const int32_t*>(ids.const_data_ptr()), ids.numel(), (uint32_t)experts,

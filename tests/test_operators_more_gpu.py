@@ -130,3 +130,57 @@ def test_plans_of_two_threads_with_different_expert_counts():
     for t in threads:
         t.join()
     assert sorted(out) == [(400, 0, True, True)] * 2 + [(1024, 0, True, True)] * 2
+
+
+def test_results_on_another_stream_do_not_take_memory_that_the_current_one_still_reads():
+    """A tensor freed while the current stream's queue still holds its readers:
+    its memory is that stream's to use again, and no other's."""
+    T, k, E, H = 4096, 4, 64, 128
+    logits, x = torch.randn(T, E, device="cuda"), torch.randn(T, H, device="cuda").bfloat16()
+    w, ids = zc.moe_route(logits, k)
+    plan = zc.moe_plan(ids, E)
+    rows = zc.moe_dispatch(x, plan.slots)
+    gy, gw = torch.randn_like(x), torch.randn_like(w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    calls = (lambda: zc.moe_route(logits, k, stream=side), lambda: [zc.moe_route_backward(gw, logits, ids, stream=side)],
+             lambda: zc.moe_plan(ids, E, stream=side), lambda: [zc.moe_dispatch(x, plan.slots, stream=side)],
+             lambda: [zc.moe_dispatch_backward(rows, plan.slots, stream=side)],
+             lambda: [zc.moe_combine(rows, plan.slots, w, stream=side)],
+             lambda: zc.moe_combine_backward(gy, rows, plan.slots, w, stream=side))
+    for call in calls:
+        sizes = [t.nbytes for t in call()]
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        freed = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+        held = {t.untyped_storage().data_ptr(): t.nbytes for t in freed}
+        del freed
+        got = call()
+        for t in got:
+            assert not any(a <= t.data_ptr() < a + n for a, n in held.items())
+        # and on the current stream they are used again, as ever
+        at = torch.empty(sizes[0], dtype=torch.uint8, device="cuda").data_ptr()
+        assert at in held
+        torch.cuda.synchronize()
+
+
+def test_results_freed_while_the_current_stream_reads_them_are_not_written_by_the_other():
+    """A result read by the current stream, freed, and the same call again: the
+    first one's readers are still queued, so the second's memory is another."""
+    logits = torch.randn(4096, 64, device="cuda")
+    other = -logits                           # every kernel is loaded before: loading one may wait for all
+    want = zc.moe_route(logits, 4)[0].double().sum()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    w, ids = zc.moe_route(logits, 4, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    first = {w.data_ptr(), ids.data_ptr()}
+    torch.cuda._sleep(200_000_000)            # a tenth of a second: kernels queued before the reader
+    read = w.double().sum()
+    done = torch.cuda.Event()
+    done.record()
+    del w, ids
+    w, ids = zc.moe_route(other, 4, stream=side)
+    assert not done.query()
+    assert not first & {w.data_ptr(), ids.data_ptr()}
+    assert torch.equal(read, want)
