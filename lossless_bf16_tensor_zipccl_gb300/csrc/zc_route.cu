@@ -61,15 +61,22 @@ __device__ __forceinline__ uint32_t first_lane(bool x) {
   return __ffs(who) - 1;
 }
 
-// The hardware's reciprocal (1 ulp) of a number that is at least 1: a score is
-// off by 2 ulp with it, and it takes one instruction where a division takes 10.
-// What is below the smallest normal float becomes 0.
-__device__ __forceinline__ float quick_rcp(float x) {
+// Reciprocal of a number from 1 to 2: the hardware's approximation (1 ulp) and a
+// step of Newton's iteration, y + y (1 - x y), which squares its error: half a
+// unit in the last place is left.  Four instructions; an IEEE division has 10
+// for the cases that do not come up here (8,192 tokens of 256 sigmoids: 8.7 us
+// with it, 8.1 like this, 7.9 with the approximation alone).
+__device__ __forceinline__ float rcp_1_to_2(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+  return fmaf(y, fmaf(-x, y, 1.0f), y);
 }
-__device__ __forceinline__ float sigmoid(float l) { return quick_rcp(1.0f + expf(-l)); }
+// 1 / (1 + e^-l), below 0 as e^l / (1 + e^l): neither overflows, so scores keep
+// their value and order down to the smallest float (l = -103).
+__device__ __forceinline__ float sigmoid(float l) {
+  const float e = expf(-fabsf(l));
+  return (l < 0.0f ? e : 1.0f) * rcp_1_to_2(1.0f + e);
+}
 
 // V values of a row from place e0 on; -inf where the row has ended.  `wide`:
 // every row starts and ends at a multiple of 16 bytes.
@@ -110,7 +117,7 @@ __device__ __forceinline__ void softmax(const float (&l)[V], float (&s)[V], floa
     z += s[j];
   }
   z = lanes_sum<L>(z);
-  const float inv = z > 0.0f ? quick_rcp(z) : 0.0f;  // 0: no eligible expert
+  const float inv = z > 0.0f ? 1.0f / z : 0.0f;  // 0: no eligible expert
 #pragma unroll
   for (int j = 0; j < V; ++j) s[j] *= inv;
   *top = m;

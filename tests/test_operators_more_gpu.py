@@ -184,3 +184,43 @@ def test_results_freed_while_the_current_stream_reads_them_are_not_written_by_th
     assert not done.query()
     assert not first & {w.data_ptr(), ids.data_ptr()}
     assert torch.equal(read, want)
+
+
+
+
+# ------------------------------------------------------------------ scores far below and above 0
+def sigmoid64(l):
+    l = l.double()
+    return torch.where(l < 0, l.exp() / (1 + l.exp()), 1 / (1 + (-l).exp()))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k", [(6, 4), (64, 9), (256, 8)])
+def test_route_sigmoid_scores_down_to_the_smallest_float(E, k, dtype):
+    """Logits from -85 to -100, where scores leave the normal floats (-87.3) and
+    e^-l the finite ones (-88.7): each keeps its rank and its value.  A score is
+    off by two units in the last place of the exponential (4 u of itself, or two
+    steps of 2^-149 among the subnormal ones), the sum's and the quotient's
+    rounding (2 u, or half a step): 7 u and 3 steps.  Neighbours are 18 steps
+    apart or more."""
+    step = 1.0 if dtype == torch.bfloat16 else 0.5
+    far = -85.0 - step * torch.arange(round(15 / step) + 1)
+    gen = torch.Generator().manual_seed(E)
+    rows = [torch.cat([far[torch.randperm(len(far), generator=gen)][:k], torch.full((E - k,), -200.0)])
+            [torch.randperm(E, generator=gen)] for _ in range(30)]
+    l = torch.stack(rows).to(dtype).cuda()
+    s = sigmoid64(l)
+    want = s.argsort(dim=1, descending=True, stable=True)[:, :k]
+    bias = torch.zeros(E, device="cuda")
+    ws = s.gather(1, want)
+    tol = 7 * U * ws + 3 * 2.0 ** -149
+    for b in (bias, None):
+        w, ids = zc.moe_route(l, k, score="sigmoid", bias=b, renormalize=False)
+        assert torch.equal(ids.long(), want)
+        assert ((w.double() - ws).abs() <= tol).all()
+        # the quotient: its terms' errors, k additions and a division
+        w, ids = zc.moe_route(l, k, score="sigmoid", bias=b)
+        total = ws.sum(1, keepdim=True)
+        q = ws / total
+        assert torch.equal(ids.long(), want)
+        assert ((w.double() - q).abs() <= tol / total + q * (tol.sum(1, keepdim=True) / total) * 1.01 + (k + 2) * U * q).all()
