@@ -343,6 +343,8 @@ typedef struct {
  *   experts  the top_k largest c_e in the kept groups, in descending order
  *            (equal: lower expert)
  *   weight   scale * s_e, or scale * s_e / sum of the chosen s
+ * Where neither a bias nor group sums enter, the logits choose: the order of the
+ * scores without their rounding.
  * The bias takes part in the choice only.  An expert whose logit is -infinite
  * or NaN, or whose c_e is, is not eligible and takes no part in the softmax
  * (the latter: in the choice); d_mask (tokens bytes, or NULL) excludes the

@@ -210,9 +210,11 @@ __global__ void __launch_bounds__(kRouteThreads) zc_route_kernel(RouteArgs a) {
     for (int j = 0; j < V; ++j) l[j] = -INFINITY;
   }
   settle(l);
-  const bool by_logit = a.softmax && !a.bias && (a.groups == 1 || !a.top2);
+  // either score grows with the logit: where nothing is added to it, the logits
+  // choose, and two that score alike in 32 bits (sigmoids are 1 from 17 on) are told apart
+  const bool by_logit = !a.bias && (a.groups == 1 || !a.top2);
   if (a.softmax && (!by_logit || !a.renormalize)) softmax<L, V>(l, c, &top, &inv);
-  if (!a.softmax) {
+  if (!a.softmax && !by_logit) {
 #pragma unroll
     for (int j = 0; j < V; ++j) c[j] = sigmoid(l[j]);
   }

@@ -224,3 +224,25 @@ def test_route_sigmoid_scores_down_to_the_smallest_float(E, k, dtype):
         q = ws / total
         assert torch.equal(ids.long(), want)
         assert ((w.double() - q).abs() <= tol / total + q * (tol.sum(1, keepdim=True) / total) * 1.01 + (k + 2) * U * q).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 4, 5])
+def test_route_without_bias_tells_apart_what_scores_alike(score, groups, dtype):
+    """Logits whose 32-bit scores are all 1, or all 0: the largest logits are
+    chosen, in order, not the lowest experts."""
+    E, k = 20 * groups, 6
+    gen = torch.Generator().manual_seed(groups)
+    for lo, step in ((20.0, 0.5), (-300.0, 1.0)):
+        values = lo + step * torch.arange(E)
+        l = torch.stack([values[torch.randperm(E, generator=gen)] for _ in range(40)]).to(dtype)
+        kept = max(1, groups - 2)
+        best = l.view(40, groups, -1).amax(-1).argsort(dim=1, descending=True, stable=True)[:, :kept]
+        allowed = torch.zeros(40, groups, dtype=torch.bool).scatter(1, best, True).repeat_interleave(20, 1)
+        want = torch.where(allowed, l.double(), -torch.inf).argsort(dim=1, descending=True, stable=True)[:, :k]
+        w, ids = zc.moe_route(l.cuda(), k, score=score, groups=groups, groups_kept=kept)
+        assert torch.equal(ids.cpu().long(), want)
+        if score == "sigmoid":
+            # u of the quotient of equal scores, for each of 1 / k and the sum
+            assert torch.allclose(w.cpu(), torch.full((40, k), 1 / k if lo > 0 else 0.0), rtol=4 * U, atol=0)
