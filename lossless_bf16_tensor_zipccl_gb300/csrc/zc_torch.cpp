@@ -328,10 +328,12 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A list of tensors, read once (it may be an iterator) and held with its
+// tensors until it goes; None: an empty one.
 struct Sequence {
   PyObject* o;
   Py_ssize_t n;
-  Sequence(PyObject* s, const char* what) : o(PySequence_Fast(s, "expected a sequence of tensors")) {
+  explicit Sequence(PyObject* s) : o(s == Py_None ? PyTuple_New(0) : PySequence_Fast(s, "expected a sequence of tensors")) {
     if (!o) throw python_error();
     n = PySequence_Fast_GET_SIZE(o);
   }
@@ -341,9 +343,8 @@ struct Sequence {
 };
 
 // The addresses of one list of tensors, into one field of the records.
-void column(PyObject* list, std::vector<zipccl_adamw_tensor>& records, bool scales, ScalarType type, c10::Device device,
+void column(const Sequence& s, std::vector<zipccl_adamw_tensor>& records, bool scales, ScalarType type, c10::Device device,
             const char* what, void (*set)(zipccl_adamw_tensor&, void*)) {
-  const Sequence s(list, what);
   if (s.n != (Py_ssize_t)records.size())
     refuse(PyExc_ValueError, "%s: expected %zd tensors, got %zd", what, (Py_ssize_t)records.size(), s.n);
   for (Py_ssize_t i = 0; i < s.n; ++i) {
@@ -362,36 +363,29 @@ void column(PyObject* list, std::vector<zipccl_adamw_tensor>& records, bool scal
 PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 15);
-  std::vector<zipccl_adamw_tensor> records;
-  ScalarType ptype, gtype;
-  std::optional<c10::Device> first;
-  {
-    const Sequence p(a[0], "params"), g(a[1], "grads");
-    if (p.n == 0) Py_RETURN_NONE;
-    if (g.n != p.n) refuse(PyExc_ValueError, "grads: expected %zd tensors, got %zd", p.n, g.n);
-    const Tensor &p0 = p.at(0, "params"), &g0 = g.at(0, "grads");
-    ptype = p0.scalar_type();
-    gtype = g0.scalar_type();
-    for (ScalarType t : {ptype, gtype})
-      if (t != ScalarType::Float && t != ScalarType::BFloat16)
-        refuse(PyExc_TypeError, "params and grads: expected float32 or bfloat16, got %s", toString(t));
-    first = cuda_device(p0, "params");
-    records.resize(p.n);
-    for (Py_ssize_t i = 0; i < p.n; ++i) records[i] = {}, records[i].n = (uint64_t)p.at(i, "params").numel();
-  }
-  const c10::Device device = *first;
+  const Sequence p(a[0]), g(a[1]), m(a[2]), v(a[3]), ms(a[4]), vs(a[5]), copies(a[6]);
+  if (p.n == 0) Py_RETURN_NONE;
+  if (g.n != p.n) refuse(PyExc_ValueError, "grads: expected %zd tensors, got %zd", p.n, g.n);
+  const Tensor &p0 = p.at(0, "params"), &g0 = g.at(0, "grads");
+  const ScalarType ptype = p0.scalar_type(), gtype = g0.scalar_type();
+  for (ScalarType t : {ptype, gtype})
+    if (t != ScalarType::Float && t != ScalarType::BFloat16)
+      refuse(PyExc_TypeError, "params and grads: expected float32 or bfloat16, got %s", toString(t));
+  const c10::Device device = cuda_device(p0, "params");
+  std::vector<zipccl_adamw_tensor> records(p.n);
+  for (Py_ssize_t i = 0; i < p.n; ++i) records[i].n = (uint64_t)p.at(i, "params").numel();
   const bool small = a[4] != Py_None;
   const ScalarType state = small ? ScalarType::Float8_e4m3fn : ScalarType::Float;
-  column(a[0], records, false, ptype, device, "params", [](zipccl_adamw_tensor& r, void* p) { r.d_param = p; });
-  column(a[1], records, false, gtype, device, "grads", [](zipccl_adamw_tensor& r, void* p) { r.d_grad = p; });
-  column(a[2], records, false, state, device, "exp_avgs", [](zipccl_adamw_tensor& r, void* p) { r.d_exp_avg = p; });
-  column(a[3], records, false, state, device, "exp_avg_sqs", [](zipccl_adamw_tensor& r, void* p) { r.d_exp_avg_sq = p; });
+  column(p, records, false, ptype, device, "params", [](zipccl_adamw_tensor& r, void* at) { r.d_param = at; });
+  column(g, records, false, gtype, device, "grads", [](zipccl_adamw_tensor& r, void* at) { r.d_grad = at; });
+  column(m, records, false, state, device, "exp_avgs", [](zipccl_adamw_tensor& r, void* at) { r.d_exp_avg = at; });
+  column(v, records, false, state, device, "exp_avg_sqs", [](zipccl_adamw_tensor& r, void* at) { r.d_exp_avg_sq = at; });
   if (small) {
-    column(a[4], records, true, ScalarType::Float, device, "scales", [](zipccl_adamw_tensor& r, void* p) { r.d_avg_scale = (float*)p; });
-    column(a[5], records, true, ScalarType::Float, device, "scales", [](zipccl_adamw_tensor& r, void* p) { r.d_sq_scale = (float*)p; });
+    column(ms, records, true, ScalarType::Float, device, "scales", [](zipccl_adamw_tensor& r, void* at) { r.d_avg_scale = (float*)at; });
+    column(vs, records, true, ScalarType::Float, device, "scales", [](zipccl_adamw_tensor& r, void* at) { r.d_sq_scale = (float*)at; });
   }
   if (a[6] != Py_None)
-    column(a[6], records, false, ScalarType::BFloat16, device, "copies", [](zipccl_adamw_tensor& r, void* p) { r.d_copy = p; });
+    column(copies, records, false, ScalarType::BFloat16, device, "copies", [](zipccl_adamw_tensor& r, void* at) { r.d_copy = at; });
   const float* scale = nullptr;
   if (a[7] != Py_None) {
     const Tensor& t = tensor(a[7], "grad_scale");

@@ -143,7 +143,7 @@ def adamw_state(param, bits: int = 32):
 
 def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step: int, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,
                weight_decay: float = 0.01, scales=None, copies=None, grad_scale=None, stream=None) -> None:
-    """One AdamW step over lists of tensors, in place (see zipccl_adamw_step).
+    """One AdamW step over lists (or iterators) of tensors, in place (see zipccl_adamw_step).
     params and grads: float32 or bfloat16, one type for each list; exp_avgs and
     exp_avg_sqs: float32, or float8_e4m3fn with ``scales`` = (avg_scales,
     sq_scales), lists of float32 [ceil(n / 256)] (``adamw_state`` makes either;

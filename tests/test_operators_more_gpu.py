@@ -246,3 +246,23 @@ def test_route_without_bias_tells_apart_what_scores_alike(score, groups, dtype):
         if score == "sigmoid":
             # u of the quotient of equal scores, for each of 1 / k and the sum
             assert torch.allclose(w.cpu(), torch.full((40, k), 1 / k if lo > 0 else 0.0), rtol=4 * U, atol=0)
+
+
+# ------------------------------------------------------------------ AdamW, its lists
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_takes_iterators(bits):
+    """model.parameters() is one: each list is read once."""
+    torch.manual_seed(3)
+    sizes = (1, 300, 4096)
+    p = [torch.randn(n, device="cuda") for n in sizes]
+    g = [torch.randn(n, device="cuda") for n in sizes]
+    results = []
+    for form in (list, iter, lambda x: (t for t in x), tuple):
+        q = [t.clone() for t in p]
+        states = list(zip(*(zc.adamw_state(t, bits) for t in q)))
+        copies = [torch.empty_like(t, dtype=torch.bfloat16) for t in q]
+        scales = None if bits == 32 else (form(states[2]), form(states[3]))
+        zc.adamw_step(form(q), form(g), form(states[0]), form(states[1]), scales=scales, copies=form(copies), step=1, lr=1e-2)
+        results.append(torch.cat(q))
+        assert torch.equal(torch.cat(copies), results[-1].bfloat16())
+    assert all(torch.equal(r, results[0]) for r in results) and not torch.equal(results[0], torch.cat(p))
