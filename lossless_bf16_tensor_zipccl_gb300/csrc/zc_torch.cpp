@@ -128,8 +128,15 @@ struct Call {
   }
 };
 
+// Autograd learns of what was written through a pointer: a tensor that it has
+// saved is then known to have changed.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* answer(zipccl_status st, std::initializer_list<Tensor> out) {
   if (st != ZIPCCL_OK) return PyLong_FromLong(st);
+  for (const Tensor& t : out) written(t);
   if (out.size() == 1) return THPVariable_Wrap(*out.begin());
   PyObject* all = PyTuple_New((Py_ssize_t)out.size());
   if (!all) throw python_error();
@@ -399,6 +406,8 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
       zipccl_adamw_step(records.data(), (uint32_t)records.size(), ptype == ScalarType::Float ? ZIPCCL_TYPE_F32 : ZIPCCL_TYPE_BF16,
                         gtype == ScalarType::Float ? ZIPCCL_TYPE_F32 : ZIPCCL_TYPE_BF16, small ? 8 : 32, &o, scale, call.stream);
   if (st != ZIPCCL_OK) return PyLong_FromLong(st);
+  for (const Sequence* s : {&p, &m, &v, &ms, &vs, &copies})
+    for (Py_ssize_t i = 0; i < s->n; ++i) written(s->at(i, "params"));
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }

@@ -266,3 +266,42 @@ def test_adamw_takes_iterators(bits):
         results.append(torch.cat(q))
         assert torch.equal(torch.cat(copies), results[-1].bfloat16())
     assert all(torch.equal(r, results[0]) for r in results) and not torch.equal(results[0], torch.cat(p))
+
+
+# ------------------------------------------------------------------ autograd
+def test_what_a_call_writes_counts_as_changed():
+    """The version that autograd compares for a tensor it has saved."""
+    T, k, E, H = 6, 2, 8, 16
+    x, l = torch.randn(T, H, device="cuda"), torch.randn(T, E, device="cuda")
+    new = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+    i32 = lambda *s: new(*s, dtype=torch.int32)  # noqa: E731
+    w, ids, counts, offsets, slots = new(T, k), i32(T, k), i32(E), i32(E + 1), i32(T, k)
+    gl, rows, gx, y, gr, gw = new(T, E), new(T * k, H), new(T, H), new(T, H), new(T * k, H), new(T, k)
+
+    def changed(call, *tensors):
+        before = [t._version for t in tensors]
+        call()
+        assert all(t._version > b for t, b in zip(tensors, before))
+
+    changed(lambda: zc.moe_route(l, k, weights=w, ids=ids), w, ids)
+    changed(lambda: zc.moe_plan(ids, E, counts=counts, offsets=offsets, slots=slots), counts, offsets, slots)
+    changed(lambda: zc.moe_dispatch(x, slots, out=rows), rows)
+    changed(lambda: zc.moe_combine(rows, slots, w, out=y), y)
+    changed(lambda: zc.moe_combine_backward(y, rows, slots, w, grad_rows=gr, grad_weights=gw), gr, gw)
+    changed(lambda: zc.moe_dispatch_backward(gr, slots, out=gx), gx)
+    changed(lambda: zc.moe_route_backward(gw, l, ids, grad_logits=gl), gl)
+    for bits in (32, 8):
+        p = torch.nn.Parameter(torch.randn(300, device="cuda"))
+        copy = torch.empty(300, dtype=torch.bfloat16, device="cuda")
+        s = zc.adamw_state(p, bits)
+        changed(lambda: zc.adamw_step([p], [x.new_ones(300)], [s[0]], [s[1]], copies=[copy], step=1, lr=1e-2,
+                                      scales=None if bits == 32 else ([s[2]], [s[3]])), p, copy, *s)
+    a = torch.ones(T, H, device="cuda", requires_grad=True)
+    loss = (a * y).sum()                      # saves y
+    zc.moe_combine(rows, slots, w, out=y)
+    with pytest.raises(RuntimeError):
+        loss.backward()
+    with torch.inference_mode():
+        z = torch.empty(T, H, device="cuda")
+        assert torch.equal(zc.moe_combine(rows, slots, w, out=z), zc.moe_combine(rows, slots, w))
+    zc.moe_combine(rows, slots, w, out=z)     # an inference tensor has no version
