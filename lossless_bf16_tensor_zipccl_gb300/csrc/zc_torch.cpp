@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -66,6 +67,19 @@ const Tensor& plain(const Tensor& t, ScalarType type, IntArrayRef shape, c10::De
 
 const void* optional(PyObject* o, ScalarType type, IntArrayRef shape, c10::Device device, const char* what) {
   return o == Py_None ? nullptr : plain(tensor(o, what), type, shape, device, what).const_data_ptr();
+}
+
+// A warning where autograd would expect to go through the call: results carry
+// no gradient, so a training step would leave out what comes before in silence.
+void no_autograd(const char* call, std::initializer_list<PyObject*> operands) {
+  if (!at::GradMode::is_enabled()) return;
+  for (PyObject* o : operands)
+    if (THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad()) {
+      if (PyErr_WarnFormat(PyExc_UserWarning, 2, "%s: an operand requires a gradient, and the results carry none: the package's "
+                           "_backward calls compute it (call under torch.no_grad() or with detached tensors)", call) < 0)
+        throw python_error();
+      return;
+    }
 }
 
 void two_dims(const Tensor& t, const char* what) {
@@ -168,6 +182,7 @@ zipccl_route_options route_options(PyObject* const* a) {
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 13);
+  no_autograd("moe_route", {a[0]});
   const zipccl_route_options o = route_options(a + 1);
   const Tensor& logits = tensor(a[0], "logits");
   const int type = value_type(logits, "logits");
@@ -194,6 +209,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 8);
+  no_autograd("moe_route_backward", {a[0], a[1]});
   const Tensor& logits = tensor(a[1], "logits");
   const int type = value_type(logits, "logits");
   const uint64_t stride = row_stride(logits, "logits");
@@ -256,6 +272,7 @@ const int32_t* pair_slots(const Tensor& slots, int64_t tokens, c10::Device devic
 PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 4);
+  no_autograd("moe_dispatch", {a[0]});
   const Tensor &x = tensor(a[0], "x"), &slots = tensor(a[1], "slots");
   const int type = value_type(x, "x");
   const uint64_t stride = row_stride(x, "x");
@@ -291,6 +308,7 @@ struct Pairs {
 PyObject* dispatch_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 4);
+  no_autograd("moe_dispatch_backward", {a[0]});
   const Pairs p(a[0], a[1], "grad_rows");
   const Call call(p.rows.device(), a[3]);
   const Tensor out = call.result(a[2], {p.tokens, p.hidden}, p.rows.scalar_type(), "out");
@@ -304,6 +322,7 @@ PyObject* dispatch_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 6);
+  no_autograd("moe_combine", {a[0], a[2], a[3]});
   const Pairs p(a[0], a[1], "rows");
   const c10::Device device = p.rows.device();
   const void* weights = optional(a[2], ScalarType::Float, {p.tokens, p.k}, device, "weights");
@@ -320,6 +339,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 7);
+  no_autograd("moe_combine_backward", {a[0], a[1], a[3]});
   const Pairs p(a[1], a[2], "rows");
   const ScalarType type = p.rows.scalar_type();
   const c10::Device device = p.rows.device();

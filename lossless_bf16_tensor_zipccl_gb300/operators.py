@@ -12,7 +12,11 @@ They are the ``zipccl_moe_*`` and ``zipccl_adamw_step`` calls of
 rest of the package they run on the current stream unless ``stream`` is given,
 allocate their results unless these are passed in, raise ``TypeError`` /
 ``ValueError`` for tensors they cannot take and ``ZipcclError`` for what the
-library refuses.
+library refuses.  Autograd does not go through them: results carry no gradient
+(a call that it would expect to go through warns), the ``_backward`` calls
+compute gradients, and what is written in place counts as changed.  Results
+allocated for another ``stream`` may be read by the current one after it has
+waited for that stream.
 """
 from __future__ import annotations
 

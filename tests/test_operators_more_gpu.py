@@ -4,6 +4,7 @@ at each test; u = 2^-24 is half a unit in the last place of a float."""
 from __future__ import annotations
 
 import threading
+import warnings
 
 import pytest
 
@@ -305,3 +306,33 @@ def test_what_a_call_writes_counts_as_changed():
         z = torch.empty(T, H, device="cuda")
         assert torch.equal(zc.moe_combine(rows, slots, w, out=z), zc.moe_combine(rows, slots, w))
     zc.moe_combine(rows, slots, w, out=z)     # an inference tensor has no version
+
+
+def test_operands_that_require_a_gradient_are_warned_of():
+    T, k, E, H = 6, 2, 8, 16
+    l, x = torch.randn(T, E, device="cuda"), torch.randn(T, H, device="cuda")
+    w, ids = zc.moe_route(l, k)
+    slots = zc.moe_plan(ids, E).slots
+    rows = zc.moe_dispatch(x, slots)
+    need = lambda t: t.clone().requires_grad_()  # noqa: E731
+    calls = {"moe_route:": lambda f: zc.moe_route(f(l), k), "moe_route_backward:": lambda f: zc.moe_route_backward(f(w), l, ids),
+             "moe_dispatch:": lambda f: zc.moe_dispatch(f(x), slots),
+             "moe_dispatch_backward:": lambda f: zc.moe_dispatch_backward(f(rows), slots),
+             "moe_combine:": lambda f: zc.moe_combine(rows, slots, f(w)),
+             "moe_combine_backward:": lambda f: zc.moe_combine_backward(f(x), rows, slots, w)}
+    for name, call in calls.items():
+        with pytest.warns(UserWarning, match=name) as caught:
+            call(need)
+        assert caught[0].filename == __file__
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            call(lambda t: t.clone())
+            call(lambda t: need(t).detach())
+            with torch.no_grad():
+                call(need)
+            p = torch.nn.Parameter(torch.randn(50, device="cuda"))     # a step is no part of a graph
+            zc.adamw_step([p], [torch.ones(50, device="cuda")], *([t] for t in zc.adamw_state(p)), step=1, lr=1e-2)
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            with pytest.raises(UserWarning):
+                call(need)
