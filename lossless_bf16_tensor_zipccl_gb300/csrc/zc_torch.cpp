@@ -148,6 +148,11 @@ void written(const Tensor& t) {
   if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
+// Pairs of a token that no call takes: refused before results of their size are
+// allocated or the count is cut to 32 bits.
+bool bad_top_k(int64_t k) { return k < 1 || k > 32; }
+PyObject* refused() { return PyLong_FromLong(ZIPCCL_ERR_INVALID_ARG); }
+
 PyObject* answer(zipccl_status st, std::initializer_list<Tensor> out) {
   if (st != ZIPCCL_OK) return PyLong_FromLong(st);
   for (const Tensor& t : out) written(t);
@@ -188,6 +193,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int type = value_type(logits, "logits");
   const uint64_t stride = row_stride(logits, "logits");
   const int64_t tokens = logits.size(0), experts = logits.size(1), k = o.top_k;
+  if (bad_top_k(k)) return refused();
   const c10::Device device = logits.device();
   const void* bias = optional(a[8], ScalarType::Float, {experts}, device, "bias");
   const void* mask = nullptr;
@@ -216,6 +222,7 @@ PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& ids = tensor(a[2], "ids");
   two_dims(ids, "ids");
   const int64_t tokens = logits.size(0), experts = logits.size(1), k = ids.size(1);
+  if (bad_top_k(k)) return refused();
   const c10::Device device = logits.device();
   plain(ids, ScalarType::Int, {tokens, k}, device, "ids");
   const Tensor& grad = plain(tensor(a[0], "grad_weights"), ScalarType::Float, {tokens, k}, device, "grad_weights");
@@ -264,7 +271,6 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 const int32_t* pair_slots(const Tensor& slots, int64_t tokens, c10::Device device) {
-  two_dims(slots, "slots");
   return static_cast<const int32_t*>(plain(slots, ScalarType::Int, {tokens, slots.size(1)}, device, "slots").const_data_ptr());
 }
 
@@ -277,6 +283,8 @@ PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int type = value_type(x, "x");
   const uint64_t stride = row_stride(x, "x");
   const int64_t tokens = x.size(0), hidden = x.size(1);
+  two_dims(slots, "slots");
+  if (bad_top_k(slots.size(1))) return refused();
   const int32_t* at = pair_slots(slots, tokens, x.device());
   const Call call(x.device(), a[3]);
   const Tensor out = call.result(a[2], {tokens * slots.size(1), hidden}, x.scalar_type(), "out");
@@ -310,6 +318,7 @@ PyObject* dispatch_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   count(n, 4);
   no_autograd("moe_dispatch_backward", {a[0]});
   const Pairs p(a[0], a[1], "grad_rows");
+  if (bad_top_k(p.k)) return refused();
   const Call call(p.rows.device(), a[3]);
   const Tensor out = call.result(a[2], {p.tokens, p.hidden}, p.rows.scalar_type(), "out");
   return answer(zipccl_moe_dispatch_backward(p.rows.const_data_ptr(), p.type, p.tokens, (uint32_t)p.k, p.hidden, p.at,
@@ -324,6 +333,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   count(n, 6);
   no_autograd("moe_combine", {a[0], a[2], a[3]});
   const Pairs p(a[0], a[1], "rows");
+  if (bad_top_k(p.k)) return refused();
   const c10::Device device = p.rows.device();
   const void* weights = optional(a[2], ScalarType::Float, {p.tokens, p.k}, device, "weights");
   const void* residual = optional(a[3], p.rows.scalar_type(), {p.tokens, p.hidden}, device, "residual");
@@ -341,6 +351,7 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   count(n, 7);
   no_autograd("moe_combine_backward", {a[0], a[1], a[3]});
   const Pairs p(a[1], a[2], "rows");
+  if (bad_top_k(p.k)) return refused();
   const ScalarType type = p.rows.scalar_type();
   const c10::Device device = p.rows.device();
   const Tensor& grad = plain(tensor(a[0], "grad_out"), type, {p.tokens, p.hidden}, device, "grad_out");

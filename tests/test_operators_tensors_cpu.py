@@ -58,3 +58,20 @@ OTHER_DEVICE = {
 def test_operands_on_another_device_are_refused_before_anything_runs(what):
     with pytest.raises(ValueError):
         OTHER_DEVICE[what]()
+
+
+@pytest.mark.parametrize("k", [0, 33, 1 << 31, (1 << 32) + 2])
+def test_pairs_of_a_token_that_no_call_takes_are_refused_before_anything_is_allocated(k):
+    """The library's own refusal, however many: a count past 32 bits is not cut, and no
+    result of that size is asked for."""
+    T, H = 3, 1
+    ids, slots, w = here(T, k, dtype=I32), here(T, k, dtype=I32), here(T, k)
+    calls = [lambda: zc.moe_route_backward(w, here(T, 8), ids), lambda: zc.moe_dispatch(here(T, H), slots),
+             lambda: zc.moe_dispatch_backward(here(T * k, H), slots), lambda: zc.moe_combine(here(T * k, H), slots),
+             lambda: zc.moe_combine_backward(here(T, H), here(T * k, H), slots)]
+    if k:
+        calls.append(lambda: zc.moe_route(here(T, 8), k))
+    for call in calls:
+        with pytest.raises(zc.ZipcclError) as e:
+            call()
+        assert e.value.status == zc.ERR_INVALID_ARG
