@@ -324,19 +324,24 @@ def _words(x):
 
 
 def _ws(nbytes: int, device, ws=None, stream=None):
-    torch = _torch()
     if ws is not None and ws.numel() >= nbytes:
         return ws
-    return _keep(torch.empty(max(256, nbytes), dtype=torch.uint8, device=device), stream)
+    return _new(max(256, nbytes), _torch().uint8, device, stream, read=False)
 
 
-def _keep(t, stream):
-    """A tensor allocated here and used by work on `stream`: when that is not
-    the current stream, the caching allocator must not hand its memory out
-    again before the work on `stream` is done."""
+def _new(n: int, dtype, device, stream, read: bool = True):
+    """n values for the work on `stream` (None: the current one), from the
+    memory of that stream: what the current stream has freed it may still be
+    reading.  One that the current stream is to `read` goes back only after
+    what that stream has queued when it is freed."""
     torch = _torch()
-    if stream is not None and stream != torch.cuda.current_stream(t.device):
-        t.record_stream(stream)
+    if stream is None or stream == torch.cuda.current_stream(device):
+        return torch.empty(n, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(n, dtype=dtype, device=device)
+    if read:
+        t.record_stream(current)
     return t
 
 
@@ -353,9 +358,9 @@ def compress(x, chunk_elems=None, sigma_hint=None, out=None, offsets=None, ws=No
     chunk_elems = [n] if chunk_elems is None else [int(c) for c in chunk_elems]
     cap = zipccl_max_compressed_bytes(chunk_elems)
     if out is None or out.numel() < cap:
-        out = _keep(torch.empty(max(16, cap), dtype=torch.uint8, device=w.device), stream)
+        out = _new(max(16, cap), torch.uint8, w.device, stream)
     if offsets is None:
-        offsets = _keep(torch.empty(len(chunk_elems) + 1, dtype=torch.int64, device=w.device), stream)
+        offsets = _new(len(chunk_elems) + 1, torch.int64, w.device, stream)
     wsb = zipccl_compress_workspace_bytes(chunk_elems)
     ws = _ws(wsb, w.device, ws, stream)
     if send is None:
@@ -375,7 +380,7 @@ def decompress(c: Compressed, out=None, ws=None, stream=None):
     """Decompress into a bfloat16 tensor of c.n elements (bit-identical)."""
     torch = _torch()
     if out is None:
-        out = _keep(torch.empty(max(1, c.n), dtype=torch.bfloat16, device=c.data.device), stream)[: c.n]
+        out = _new(max(1, c.n), torch.bfloat16, c.data.device, stream)[: c.n]
     wsb = zipccl_decompress_workspace_bytes(c.n, c.n_chunks)
     ws = _ws(wsb, c.data.device, ws, stream)
     st = zipccl_decompress(c.data.data_ptr(), c.offsets.data_ptr(), c.n_chunks, out.data_ptr(), c.n,
@@ -391,7 +396,7 @@ def decompress_reduce(peer_chunks, n: int, out=None, ws=None, stream=None):
     k = len(peer_chunks)
     dev = peer_chunks[0].device
     if out is None:
-        out = _keep(torch.empty(max(1, n), dtype=torch.bfloat16, device=dev), stream)[:n]
+        out = _new(max(1, n), torch.bfloat16, dev, stream)[:n]
     wsb = zipccl_reduce_workspace_bytes(k)
     ws = _ws(wsb, dev, ws, stream)
     st = zipccl_decompress_reduce([p.data_ptr() for p in peer_chunks], [p.numel() for p in peer_chunks], k, n,
