@@ -336,3 +336,99 @@ def test_operands_that_require_a_gradient_are_warned_of():
             warnings.simplefilter("error")
             with pytest.raises(UserWarning):
                 call(need)
+
+
+# ------------------------------------------------------------------ AdamW, states that cancel
+def e4m3_half_step(y):
+    y = y.abs().clamp(min=2.0 ** -6)
+    return torch.exp2(torch.floor(torch.log2(y)) - 4)
+
+
+@pytest.mark.parametrize("first", [0, 3])
+@pytest.mark.parametrize("sizes", [[257, 7, 4097], [20000, 511]])
+def test_adamw_8_bit_first_moments_of_changing_gradients(sizes, first):
+    """Gradients of a new draw each step, so that first moments cancel and change
+    sign; every code and scale is checked.  m is off by 4 roundings of its two
+    terms' magnitudes (5 u with what is left of them squared); a scale by that of its block's largest value and 2
+    roundings; a code is the value nearest to m over the scale, which is off by
+    another 3 u."""
+    torch.manual_seed(len(sizes) + first)
+    flat = lambda s: list((torch.randn(first + sum(sizes), device="cuda") * s)[first:].split(sizes))  # noqa: E731
+    p = flat(0.02)
+    m, v, ms, vs = (list(x) for x in zip(*(zc.adamw_state(t, bits=8) for t in p)))
+    spread = lambda t, s, n: t.double() * s.double().repeat_interleave(256)[:n]  # noqa: E731
+    flips = 0
+    for step in range(1, 5):
+        g = flat(1e-3)
+        m0 = [spread(a.float(), s, a.numel()) for a, s in zip(m, ms)]
+        zc.adamw_step(p, g, m, v, scales=(ms, vs), step=step, lr=1e-2, betas=(0.9, 0.95))
+        for i, n in enumerate(sizes):
+            want = 0.9 * m0[i] + 0.1 * g[i].double()
+            size = 0.9 * m0[i].abs() + 0.1 * g[i].double().abs()
+            off = 5 * U * size
+            blocks = torch.nn.functional.pad(torch.stack([want.abs(), off]), (0, -n % 256)).view(2, -1, 256)
+            top, slack = blocks[0].amax(1), blocks[1].amax(1)
+            s = ms[i].double()
+            assert ((s - top / 448).abs() <= (slack + 3 * U * top) / 448 + 2.0 ** -126).all()
+            sv = s.repeat_interleave(256)[:n]
+            y = (want / sv).clamp(-448, 448)
+            code = m[i].float().double()
+            tol = (e4m3_half_step(y) + off / sv + 3 * U * y.abs()) * 1.0001
+            # where y and its rounding lie on either side of a power of two the coarser step counts
+            tol = torch.maximum(tol, (e4m3_half_step(code) + off / sv + 3 * U * y.abs()) * 1.0001)
+            assert ((code - y).abs() <= tol).all()
+            flips += int(((want * m0[i]) < 0).sum())
+    assert flips > 100                            # the draw does what the test is for
+
+
+# ------------------------------------------------------------------ rows that start anywhere
+def pairs(T, k, seed):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    ids = torch.rand(T, 3 * k, generator=gen, device="cuda").topk(k, -1).indices.int()
+    ids[torch.rand(T, k, generator=gen, device="cuda") < 0.1] = -1
+    slots = zc.moe_plan(ids, 3 * k).slots
+    return slots, gen
+
+
+ROUND = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,k,H", [(3, 2, 1), (40, 2, 7), (900, 3, 64), (300, 2, 1030), (1500, 2, 2055), (61, 4, 10007)])
+@pytest.mark.parametrize("start", [0, 1, 5])
+def test_residual_in_place_and_operands_at_any_place(T, k, H, dtype, start):
+    """Combine with the residual as its result, and both gradients, with every
+    row buffer `start` values into its memory, against 64 bits: up to 5 products
+    and sums, 2 roundings each (10 u of the magnitudes), and one to the type
+    (half a step of 2^-24 below float16's normal range)."""
+    slots, gen = pairs(T, k, T + H)
+
+    def new(n):
+        flat = torch.randn(n * H + start, generator=gen, device="cuda").to(dtype)
+        return flat[start:].view(n, H)
+    rows, y, gy = new(T * k), new(T), new(T)
+    w = torch.rand(T, k, generator=gen, device="cuda") - 0.3
+    gone = (slots < 0)[:, :, None]
+    at = torch.where(slots < 0, -1 - slots, slots).long()
+    picked = torch.where(gone, 0.0, rows[at.view(-1)].view(T, k, H).double())
+
+    def near(got, want, size):
+        tol = 10 * U * size + (0 if dtype == torch.float32 else ROUND[dtype] * want.abs() + 2.0 ** -25)
+        assert ((got.double() - want).abs() <= tol).all()
+    terms = picked * w.double()[:, :, None]
+    want, size = terms.sum(1) + y.double(), terms.abs().sum(1) + y.double().abs()
+    got = zc.moe_combine(rows, slots, w, residual=y, out=y)
+    assert got.data_ptr() == y.data_ptr()
+    near(y, want, size)
+    gx = new(T)
+    zc.moe_dispatch_backward(rows, slots, out=gx)
+    near(gx, picked.sum(1), picked.abs().sum(1))
+    gr = new(T * k)
+    _, gw = zc.moe_combine_backward(gy, rows, slots, w, grad_rows=gr)
+    back = torch.where(gone, 0.0, w.double()[:, :, None] * gy.double()[:, None, :])
+    near(gr[at.view(-1)].view(T, k, H), back, back.abs())
+    # a lane sums H / 32 products at most, or the 8 of one vector; then a tree
+    products = picked * gy.double()[:, None, :]
+    runs = max(H / 32, min(H, 8))
+    assert ((gw.double() - products.sum(-1)).abs() <= (runs + 20) * U * products.abs().sum(-1)).all()
