@@ -114,10 +114,11 @@ double real(PyObject* o) {
 // only after what that stream has queued when it is freed.
 struct Call {
   c10::Device device;
-  c10::cuda::CUDAGuard current_device;
+  c10::cuda::OptionalCUDAGuard current_device;  // left alone where the device is current already
   cudaStream_t stream;
   bool other = false;
-  Call(c10::Device d, PyObject* s) : device(d), current_device(d) {
+  Call(c10::Device d, PyObject* s) : device(d) {
+    if (c10::cuda::current_device() != d.index()) current_device.set_device(d);
     const cudaStream_t current = c10::cuda::getCurrentCUDAStream(device.index()).stream();
     stream = current;
     if (s != Py_None) {
@@ -144,8 +145,8 @@ struct Call {
 
 // Autograd learns of what was written through a pointer: a tensor that it has
 // saved is then known to have changed.
-void written(const Tensor& t) {
-  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+void written(c10::TensorImpl* t) {
+  if (!t->is_inference()) t->bump_version();
 }
 
 // Pairs of a token that no call takes: refused before results of their size are
@@ -155,7 +156,7 @@ PyObject* refused() { return PyLong_FromLong(ZIPCCL_ERR_INVALID_ARG); }
 
 PyObject* answer(zipccl_status st, std::initializer_list<Tensor> out) {
   if (st != ZIPCCL_OK) return PyLong_FromLong(st);
-  for (const Tensor& t : out) written(t);
+  for (const Tensor& t : out) written(t.unsafeGetTensorImpl());
   if (out.size() == 1) return THPVariable_Wrap(*out.begin());
   PyObject* all = PyTuple_New((Py_ssize_t)out.size());
   if (!all) throw python_error();
@@ -380,19 +381,21 @@ struct Sequence {
   const Tensor& at(Py_ssize_t i, const char* what) const { return tensor(PySequence_Fast_GET_ITEM(o, i), what); }
 };
 
-// The addresses of one list of tensors, into one field of the records.
+// The addresses of one list of tensors, into one field of the records; the
+// tensors into `changed`, unless that is null.
 void column(const Sequence& s, std::vector<zipccl_adamw_tensor>& records, bool scales, ScalarType type, c10::Device device,
-            const char* what, void (*set)(zipccl_adamw_tensor&, void*)) {
+            std::vector<c10::TensorImpl*>* changed, const char* what, void (*set)(zipccl_adamw_tensor&, void*)) {
   if (s.n != (Py_ssize_t)records.size())
     refuse(PyExc_ValueError, "%s: expected %zd tensors, got %zd", what, (Py_ssize_t)records.size(), s.n);
   for (Py_ssize_t i = 0; i < s.n; ++i) {
     const Tensor& t = s.at(i, what);
     const uint64_t want = scales ? (records[i].n + ZIPCCL_ADAMW_BLOCK - 1) / ZIPCCL_ADAMW_BLOCK : records[i].n;
     if (t.scalar_type() != type) refuse(PyExc_TypeError, "%s: expected %s, got %s", what, toString(type), toString(t.scalar_type()));
-    if (!t.is_cuda() || !t.is_contiguous()) refuse(PyExc_ValueError, "%s: expected contiguous CUDA tensors", what);
-    if (t.device() != device) refuse(PyExc_ValueError, "%s: expected tensors on the device of the first parameter", what);
+    if (t.device() != device || !t.is_contiguous())
+      refuse(PyExc_ValueError, "%s: expected contiguous tensors on the device of the first parameter", what);
     if ((uint64_t)t.numel() != want) refuse(PyExc_ValueError, "%s: a tensor of another size was expected", what);
     set(records[i], t.data_ptr());
+    if (changed) changed->push_back(t.unsafeGetTensorImpl());
   }
 }
 
@@ -411,19 +414,21 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse(PyExc_TypeError, "params and grads: expected float32 or bfloat16, got %s", toString(t));
   const c10::Device device = cuda_device(p0, "params");
   std::vector<zipccl_adamw_tensor> records(p.n);
+  std::vector<c10::TensorImpl*> changed;
+  changed.reserve(6 * p.n);
   for (Py_ssize_t i = 0; i < p.n; ++i) records[i].n = (uint64_t)p.at(i, "params").numel();
   const bool small = a[4] != Py_None;
   const ScalarType state = small ? ScalarType::Float8_e4m3fn : ScalarType::Float;
-  column(p, records, false, ptype, device, "params", [](zipccl_adamw_tensor& r, void* at) { r.d_param = at; });
-  column(g, records, false, gtype, device, "grads", [](zipccl_adamw_tensor& r, void* at) { r.d_grad = at; });
-  column(m, records, false, state, device, "exp_avgs", [](zipccl_adamw_tensor& r, void* at) { r.d_exp_avg = at; });
-  column(v, records, false, state, device, "exp_avg_sqs", [](zipccl_adamw_tensor& r, void* at) { r.d_exp_avg_sq = at; });
+  column(p, records, false, ptype, device, &changed, "params", [](zipccl_adamw_tensor& r, void* at) { r.d_param = at; });
+  column(g, records, false, gtype, device, nullptr, "grads", [](zipccl_adamw_tensor& r, void* at) { r.d_grad = at; });
+  column(m, records, false, state, device, &changed, "exp_avgs", [](zipccl_adamw_tensor& r, void* at) { r.d_exp_avg = at; });
+  column(v, records, false, state, device, &changed, "exp_avg_sqs", [](zipccl_adamw_tensor& r, void* at) { r.d_exp_avg_sq = at; });
   if (small) {
-    column(ms, records, true, ScalarType::Float, device, "scales", [](zipccl_adamw_tensor& r, void* at) { r.d_avg_scale = (float*)at; });
-    column(vs, records, true, ScalarType::Float, device, "scales", [](zipccl_adamw_tensor& r, void* at) { r.d_sq_scale = (float*)at; });
+    column(ms, records, true, ScalarType::Float, device, &changed, "scales", [](zipccl_adamw_tensor& r, void* at) { r.d_avg_scale = (float*)at; });
+    column(vs, records, true, ScalarType::Float, device, &changed, "scales", [](zipccl_adamw_tensor& r, void* at) { r.d_sq_scale = (float*)at; });
   }
   if (a[6] != Py_None)
-    column(copies, records, false, ScalarType::BFloat16, device, "copies", [](zipccl_adamw_tensor& r, void* at) { r.d_copy = at; });
+    column(copies, records, false, ScalarType::BFloat16, device, &changed, "copies", [](zipccl_adamw_tensor& r, void* at) { r.d_copy = at; });
   const float* scale = nullptr;
   if (a[7] != Py_None) {
     const Tensor& t = tensor(a[7], "grad_scale");
@@ -437,8 +442,7 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
       zipccl_adamw_step(records.data(), (uint32_t)records.size(), ptype == ScalarType::Float ? ZIPCCL_TYPE_F32 : ZIPCCL_TYPE_BF16,
                         gtype == ScalarType::Float ? ZIPCCL_TYPE_F32 : ZIPCCL_TYPE_BF16, small ? 8 : 32, &o, scale, call.stream);
   if (st != ZIPCCL_OK) return PyLong_FromLong(st);
-  for (const Sequence* s : {&p, &m, &v, &ms, &vs, &copies})
-    for (Py_ssize_t i = 0; i < s->n; ++i) written(s->at(i, "params"));
+  for (c10::TensorImpl* t : changed) written(t);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
