@@ -106,6 +106,12 @@ double real(PyObject* o) {
   return v;
 }
 
+// A tensor that the call is about to write through a pointer: autograd, where it
+// has saved it, then knows that it has changed.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // A call's device, current until the call ends: the launches go to the current
 // device, and stream 0 is that device's.  Its stream (None: the current one of
 // that device) and the results it allocates.  They come from the memory of the
@@ -118,7 +124,7 @@ struct Call {
   cudaStream_t stream;
   bool other = false;
   Call(c10::Device d, PyObject* s) : device(d) {
-    if (c10::cuda::current_device() != d.index()) current_device.set_device(d);
+    if (c10::cuda::device_count() > 1 && c10::cuda::current_device() != d.index()) current_device.set_device(d);
     const cudaStream_t current = c10::cuda::getCurrentCUDAStream(device.index()).stream();
     stream = current;
     if (s != Py_None) {
@@ -139,15 +145,12 @@ struct Call {
     return t;
   }
   Tensor result(PyObject* o, IntArrayRef shape, ScalarType type, const char* what) const {
-    return o == Py_None ? empty(shape, type) : plain(tensor(o, what), type, shape, device, what);
+    if (o == Py_None) return empty(shape, type);
+    const Tensor& t = plain(tensor(o, what), type, shape, device, what);
+    written(t);
+    return t;
   }
 };
-
-// Autograd learns of what was written through a pointer: a tensor that it has
-// saved is then known to have changed.
-void written(c10::TensorImpl* t) {
-  if (!t->is_inference()) t->bump_version();
-}
 
 // Pairs of a token that no call takes: refused before results of their size are
 // allocated or the count is cut to 32 bits.
@@ -156,7 +159,6 @@ PyObject* refused() { return PyLong_FromLong(ZIPCCL_ERR_INVALID_ARG); }
 
 PyObject* answer(zipccl_status st, std::initializer_list<Tensor> out) {
   if (st != ZIPCCL_OK) return PyLong_FromLong(st);
-  for (const Tensor& t : out) written(t.unsafeGetTensorImpl());
   if (out.size() == 1) return THPVariable_Wrap(*out.begin());
   PyObject* all = PyTuple_New((Py_ssize_t)out.size());
   if (!all) throw python_error();
@@ -381,10 +383,9 @@ struct Sequence {
   const Tensor& at(Py_ssize_t i, const char* what) const { return tensor(PySequence_Fast_GET_ITEM(o, i), what); }
 };
 
-// The addresses of one list of tensors, into one field of the records; the
-// tensors into `changed`, unless that is null.
+// The addresses of one list of tensors, into one field of the records.
 void column(const Sequence& s, std::vector<zipccl_adamw_tensor>& records, bool scales, ScalarType type, c10::Device device,
-            std::vector<c10::TensorImpl*>* changed, const char* what, void (*set)(zipccl_adamw_tensor&, void*)) {
+            bool writes, const char* what, void (*set)(zipccl_adamw_tensor&, void*)) {
   if (s.n != (Py_ssize_t)records.size())
     refuse(PyExc_ValueError, "%s: expected %zd tensors, got %zd", what, (Py_ssize_t)records.size(), s.n);
   for (Py_ssize_t i = 0; i < s.n; ++i) {
@@ -395,7 +396,7 @@ void column(const Sequence& s, std::vector<zipccl_adamw_tensor>& records, bool s
       refuse(PyExc_ValueError, "%s: expected contiguous tensors on the device of the first parameter", what);
     if ((uint64_t)t.numel() != want) refuse(PyExc_ValueError, "%s: a tensor of another size was expected", what);
     set(records[i], t.data_ptr());
-    if (changed) changed->push_back(t.unsafeGetTensorImpl());
+    if (writes) written(t);
   }
 }
 
@@ -414,21 +415,19 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse(PyExc_TypeError, "params and grads: expected float32 or bfloat16, got %s", toString(t));
   const c10::Device device = cuda_device(p0, "params");
   std::vector<zipccl_adamw_tensor> records(p.n);
-  std::vector<c10::TensorImpl*> changed;
-  changed.reserve(6 * p.n);
   for (Py_ssize_t i = 0; i < p.n; ++i) records[i].n = (uint64_t)p.at(i, "params").numel();
   const bool small = a[4] != Py_None;
   const ScalarType state = small ? ScalarType::Float8_e4m3fn : ScalarType::Float;
-  column(p, records, false, ptype, device, &changed, "params", [](zipccl_adamw_tensor& r, void* at) { r.d_param = at; });
-  column(g, records, false, gtype, device, nullptr, "grads", [](zipccl_adamw_tensor& r, void* at) { r.d_grad = at; });
-  column(m, records, false, state, device, &changed, "exp_avgs", [](zipccl_adamw_tensor& r, void* at) { r.d_exp_avg = at; });
-  column(v, records, false, state, device, &changed, "exp_avg_sqs", [](zipccl_adamw_tensor& r, void* at) { r.d_exp_avg_sq = at; });
+  column(p, records, false, ptype, device, true, "params", [](zipccl_adamw_tensor& r, void* at) { r.d_param = at; });
+  column(g, records, false, gtype, device, false, "grads", [](zipccl_adamw_tensor& r, void* at) { r.d_grad = at; });
+  column(m, records, false, state, device, true, "exp_avgs", [](zipccl_adamw_tensor& r, void* at) { r.d_exp_avg = at; });
+  column(v, records, false, state, device, true, "exp_avg_sqs", [](zipccl_adamw_tensor& r, void* at) { r.d_exp_avg_sq = at; });
   if (small) {
-    column(ms, records, true, ScalarType::Float, device, &changed, "scales", [](zipccl_adamw_tensor& r, void* at) { r.d_avg_scale = (float*)at; });
-    column(vs, records, true, ScalarType::Float, device, &changed, "scales", [](zipccl_adamw_tensor& r, void* at) { r.d_sq_scale = (float*)at; });
+    column(ms, records, true, ScalarType::Float, device, true, "scales", [](zipccl_adamw_tensor& r, void* at) { r.d_avg_scale = (float*)at; });
+    column(vs, records, true, ScalarType::Float, device, true, "scales", [](zipccl_adamw_tensor& r, void* at) { r.d_sq_scale = (float*)at; });
   }
   if (a[6] != Py_None)
-    column(copies, records, false, ScalarType::BFloat16, device, &changed, "copies", [](zipccl_adamw_tensor& r, void* at) { r.d_copy = at; });
+    column(copies, records, false, ScalarType::BFloat16, device, true, "copies", [](zipccl_adamw_tensor& r, void* at) { r.d_copy = at; });
   const float* scale = nullptr;
   if (a[7] != Py_None) {
     const Tensor& t = tensor(a[7], "grad_scale");
@@ -442,7 +441,6 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
       zipccl_adamw_step(records.data(), (uint32_t)records.size(), ptype == ScalarType::Float ? ZIPCCL_TYPE_F32 : ZIPCCL_TYPE_BF16,
                         gtype == ScalarType::Float ? ZIPCCL_TYPE_F32 : ZIPCCL_TYPE_BF16, small ? 8 : 32, &o, scale, call.stream);
   if (st != ZIPCCL_OK) return PyLong_FromLong(st);
-  for (c10::TensorImpl* t : changed) written(t);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
