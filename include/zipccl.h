@@ -428,8 +428,9 @@ zipccl_status zipccl_moe_combine_backward(const void *d_grad_y, const void *d_ro
  *   m = beta1 m + (1 - beta1) g          v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) *
  *       m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * (a divisor below 2^-126 counts as 2^-126, one of NaN makes p NaN) and, where
- * d_copy is set, d_copy = bf16(p).
+ * (a divisor below 2^-126 counts as 2^-126, one of NaN makes p NaN; the quotient
+ * is a product with the divisor's reciprocal, good to 1 ulp) and, where d_copy is
+ * set, d_copy = bf16(p).
  * param_type: F32 or BF16 (then p is rounded at every step);  grad_type: F32
  * or BF16.
  * state_bits 32: d_exp_avg and d_exp_avg_sq hold m and v as floats.

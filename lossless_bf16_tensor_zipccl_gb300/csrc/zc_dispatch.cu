@@ -35,7 +35,8 @@ struct RowArgs {
 //    bytes takes it, a vector at a time: it only stores what it has loaded
 //    once, and stores wait for nothing (16,384 x 4,096 bf16, two pairs: 61 us,
 //    99% of the measured copy rate).  Elsewhere it goes value by value: where
-//    results or the experts' rows do not start at a multiple of 16 bytes.
+//    results or the experts' rows do not start at a multiple of 16 bytes (the
+//    same size, combine: 277 us against 61).
 //  - Piped: combine and its gradient gather rows, so a warp that loads, sums
 //    and stores waits for a slot and then for a row each time, and more loads
 //    in registers cost warps (the same size: 73 and 124 us at best).  Here
