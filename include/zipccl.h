@@ -466,6 +466,81 @@ zipccl_status zipccl_adamw_step(const zipccl_adamw_tensor *tensors, uint32_t n_t
                                 int grad_type, int state_bits, const zipccl_adamw_options *options,
                                 const float *d_grad_scale, void *stream);
 
+/*
+ * ---------------------------------------------------------------- what the experts compute
+ *
+ * 8-bit blocks.  A block of values x with the largest finite magnitude a has
+ * the scale 2^e, e the smallest whole number from -127 on with a <= 448 * 2^e,
+ * and the codes E4M3(x * 2^-e), to nearest even: the scaling is exact, so the
+ * code is the only rounding.  A value that is not finite has the code of NaN,
+ * in its own place only.  Scales are bytes e + 127 (E8M0: 255 is NaN, as a
+ * block's scale may be set by others).  Codes: rows code_stride bytes apart, a
+ * multiple of 16, from a 16-byte aligned start.  At most 2^31 - 1 rows and
+ * 2^22 columns.
+ *
+ * zipccl_moe_quantize: blocks of ZIPCCL_FP8_BLOCK consecutive values of a
+ *   row.  d_x [rows][cols] of `type`, rows row_stride values apart; d_scales
+ *   [rows][ceil(cols / 128)].
+ * zipccl_moe_quantize_columns: blocks of 128 consecutive rows of a chunk in
+ *   one column; chunk e is the rows d_offsets[e] .. d_offsets[e + 1] - 1, as
+ *   zipccl_moe_plan gives them (d_offsets NULL, experts 1: all rows).  d_scales
+ *   [rows / 128 + experts][cols]: chunk by chunk, ceil(rows of the chunk / 128)
+ *   each, then zero bytes; rows behind the last chunk have codes of zero.  With
+ *   d_row_codes and d_row_scales (or NULL) also what zipccl_moe_quantize gives,
+ *   from the same reading.
+ * zipccl_moe_quantize_weights: blocks of 128 x 128.  d_w [experts][rows][cols],
+ *   contiguous; d_codes [experts][rows] rows; d_scales [experts]
+ *   [ceil(rows / 128)][ceil(cols / 128)].
+ */
+#define ZIPCCL_FP8_BLOCK 128u
+zipccl_status zipccl_moe_quantize(const void *d_x, int type, uint64_t row_stride, uint64_t rows, uint64_t cols,
+                                  uint8_t *d_codes, uint64_t code_stride, uint8_t *d_scales, void *stream);
+zipccl_status zipccl_moe_quantize_columns(const void *d_x, int type, uint64_t row_stride, uint64_t rows,
+                                          uint64_t cols, const int32_t *d_offsets, uint32_t experts,
+                                          uint8_t *d_codes, uint64_t code_stride, uint8_t *d_scales,
+                                          uint8_t *d_row_codes, uint64_t row_code_stride,
+                                          uint8_t *d_row_scales, void *stream);
+zipccl_status zipccl_moe_quantize_weights(const void *d_w, int type, uint32_t experts, uint64_t rows,
+                                          uint64_t cols, uint8_t *d_codes, uint64_t code_stride,
+                                          uint8_t *d_scales, void *stream);
+
+/*
+ * Products of the experts' chunks with their matrices, operands in 8-bit
+ * blocks, chunks as d_offsets [experts + 1] gives them (NULL with experts 1:
+ * all rows; offsets are taken from 0 on, never falling and within the rows,
+ * whatever the memory holds).  With x, w, g the values that the codes and
+ * scales stand for:
+ *   ZIPCCL_MATMUL_FORWARD   out[m][n] = sum_k x[m][k] w[e][n][k]
+ *       a: rows [rows][inner] by rows; b: weights [experts][outer][inner];
+ *       out [rows][outer]
+ *   ZIPCCL_MATMUL_BACKWARD  out[m][k] = sum_n g[m][n] w[e][n][k]
+ *       a: gradients [rows][outer] by rows; b: the same weights;
+ *       out [rows][inner]
+ *   ZIPCCL_MATMUL_WEIGHTS   out[e][n][k] = sum of g[m][n] x[m][k] over the
+ *       chunk's rows; a: gradients [rows][outer] by columns; b: rows
+ *       [rows][inner] by columns; out [experts][outer][inner]
+ * Rows behind the last chunk are zeros in `out`, as are the gradients of the
+ * weights of an empty chunk.  Sums are held in 32 bits on the tensor cores, in a
+ * fixed order; out_type F32, BF16 or F16, rounded once.  out: rows out_stride
+ * values apart, the WEIGHTS form's matrices `outer` rows apart.
+ * A wait inside the kernel that runs out (2 s; not to be expected) leaves what
+ * the block had not yet written unwritten and sets the device's word that
+ * zipccl_moe_status reads and clears: ZIPCCL_OK or ZIPCCL_ERR_TIMEOUT
+ * (synchronizes `stream`).
+ */
+typedef enum { ZIPCCL_MATMUL_FORWARD = 0, ZIPCCL_MATMUL_BACKWARD = 1, ZIPCCL_MATMUL_WEIGHTS = 2 } zipccl_matmul_form;
+
+typedef struct {
+    const uint8_t *d_codes;  /* 16-byte aligned */
+    const uint8_t *d_scales; /* contiguous, laid out as the quantizing call leaves them */
+    uint64_t stride;         /* bytes between rows of codes, a multiple of 16 */
+} zipccl_fp8_blocks;
+
+zipccl_status zipccl_moe_matmul(int form, const zipccl_fp8_blocks *a, const zipccl_fp8_blocks *b,
+                                uint64_t rows, uint64_t inner, uint64_t outer, const int32_t *d_offsets,
+                                uint32_t experts, void *d_out, int out_type, uint64_t out_stride, void *stream);
+zipccl_status zipccl_moe_status(void *stream);
+
 #ifdef __cplusplus
 }
 #endif

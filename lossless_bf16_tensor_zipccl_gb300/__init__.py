@@ -47,7 +47,8 @@ EXPORTED_SYMBOLS = [
     "zipccl_choose_compressed", "zipccl_selftest_bounded_wait", "zipccl_profile_encode_events",
     "zipccl_moe_route", "zipccl_moe_route_backward", "zipccl_moe_plan_workspace_bytes", "zipccl_moe_plan",
     "zipccl_moe_dispatch", "zipccl_moe_dispatch_backward", "zipccl_moe_combine", "zipccl_moe_combine_backward",
-    "zipccl_adamw_step",
+    "zipccl_adamw_step", "zipccl_moe_quantize", "zipccl_moe_quantize_columns", "zipccl_moe_quantize_weights",
+    "zipccl_moe_matmul", "zipccl_moe_status",
 ]
 
 _lock = threading.Lock()
@@ -409,7 +410,9 @@ from .operators_abi import *  # noqa: E402,F401,F403
 from .operators_abi import __all__ as _abi_names  # noqa: E402
 
 _tensor_names = ["MoePlan", "moe_route", "moe_route_backward", "moe_plan", "moe_dispatch", "moe_dispatch_backward",
-                 "moe_combine", "moe_combine_backward", "adamw_step", "adamw_state", "ADAMW_BLOCK"]
+                 "moe_combine", "moe_combine_backward", "adamw_step", "adamw_state", "ADAMW_BLOCK",
+                 "Fp8Blocks", "FP8_BLOCK", "moe_quantize", "moe_quantize_columns", "moe_quantize_weights",
+                 "moe_matmul", "moe_matmul_backward", "moe_matmul_backward_weights", "moe_status"]
 __all__ += [*_abi_names, *_tensor_names]
 
 

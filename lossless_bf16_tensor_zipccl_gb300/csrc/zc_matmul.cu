@@ -1,0 +1,482 @@
+// zc_matmul.cu -- products of the experts' chunks with their matrices, operands
+// in 8-bit blocks, on the tensor cores.
+//
+// All three forms are sums over one index of products of codes, times a power of
+// two for each 128 places of the index.  The tensor cores take the powers of two
+// as they are (one for 32 places of the sum: the same for four instructions), so
+// nothing is done between the operands' arrival and the result.
+//
+// A tile of the result is 128 lanes x up to 256 columns of tensor memory.  The
+// lanes are the matrices' rows (outer or inner places), the columns the chunk's
+// rows: a chunk may have any number of rows, and the columns of an instruction may
+// be any multiple of 32, so that a chunk's end costs at most 31 columns, where the
+// lanes are always full.  In the gradient of the weights lanes are the inner
+// places, columns the outer ones, and the chunk's rows are summed over.
+// The result thus lies with its contiguous index along the lanes.
+//
+// The weights are read along the sum forward and across it backward, from the
+// same codes: blocks of 128 x 128 serve both.
+//
+// Warps: 0 loads tiles through tensor maps, four stages of 128 places ahead; 1
+// issues the products; 2 lays the scales out (128 rows x 4 bytes, four blocks of
+// the sum a time); 3 clears what a chunk's last block of rows reads of the next
+// chunk (gradient of the weights); 4 to 7 write results.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "zc_fp8.cuh"
+#include "zc_tensor.cuh"
+#include "zipccl.h"
+
+namespace zc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr uint32_t kLanes = 128, kColumns = 256, kPlaces = 128;  // of a tile; places of the sum in a stage
+constexpr uint32_t kStages = 4;
+constexpr uint32_t kBytesA = kLanes * kPlaces, kBytesB = kColumns * kPlaces, kStageBytes = kBytesA + kBytesB;
+constexpr uint32_t kScaleSets = 4, kScaleBytes = 512 * 3;  // four blocks' scales: 128 lanes, 256 columns
+constexpr uint32_t kBoxRows = 32;
+constexpr uint32_t kScaleColumns = 256;  // tensor memory: where scales begin, 16 columns for each of two sets
+
+__device__ unsigned int g_wait_ran_out;
+
+struct MatmulArgs {
+  CUtensorMap a, b;
+  const uint8_t *scales_a, *scales_b;
+  const int32_t* offsets;
+  void* out;
+  uint64_t out_stride, out_matrix;       // values between rows and matrices
+  uint64_t a_matrix;                     // scales of a matrix of weights
+  uint32_t a_lane, a_block;              // bytes from a lane block's scale to the next, from a block of the sum's to the next
+  uint32_t lanes, columns, sum;          // of the result and the sum (WEIGHTS: columns; sum unused; else columns unused)
+  uint32_t rows, chunks, lane_tiles, column_tiles;
+  uint32_t b_blocks;                     // scales of a row
+};
+
+struct Shared {
+  alignas(1024) uint8_t stage[kStages][kStageBytes];
+  alignas(128) uint8_t scales[kScaleSets][kScaleBytes];
+  uint64_t full[kStages], empty[kStages], scales_full[kScaleSets], scales_empty[kScaleSets], clear, cleared, done, taken;
+  uint32_t tmem;
+  uint32_t first[kMaxChunks + 2];  // first row of each chunk; the rows behind the last are one more
+  uint32_t tiles[kMaxChunks + 2];  // tiles of rows before each (WEIGHTS: blocks of the scales)
+};
+
+struct Tile {
+  uint32_t chunk, row, count;   // rows of the tile (WEIGHTS: of the chunk)
+  uint32_t lane0, column0, columns, blocks;
+};
+
+template <bool kWeights>
+__device__ __forceinline__ Tile tile_of(const MatmulArgs& a, const Shared& s, uint32_t t) {
+  Tile x;
+  if constexpr (kWeights) {
+    const uint32_t per = a.lane_tiles * a.column_tiles;
+    x.chunk = t / per;
+    t -= x.chunk * per;
+    x.column0 = t / a.lane_tiles * kColumns;
+    x.lane0 = t % a.lane_tiles * kLanes;
+    x.row = s.first[x.chunk];
+    x.count = s.first[x.chunk + 1] - x.row;
+    x.columns = min(kColumns, a.columns - x.column0);
+    x.blocks = (x.count + kPlaces - 1) / kPlaces;
+  } else {
+    const uint32_t r = t / a.lane_tiles;
+    x.lane0 = (t - r * a.lane_tiles) * kLanes;
+    uint32_t lo = 0, hi = a.chunks + 1;  // the chunk whose tiles begin at r or before, the next one's behind it
+    while (hi - lo > 1) {
+      const uint32_t mid = (lo + hi) / 2;
+      if (s.tiles[mid] <= r) lo = mid;
+      else hi = mid;
+    }
+    x.chunk = lo;
+    const uint32_t all = s.first[lo + 1] - s.first[lo], n = s.tiles[lo + 1] - s.tiles[lo];
+    const uint32_t step = ((all + n - 1) / n + 31) / 32 * 32, from = (r - s.tiles[lo]) * step;
+    x.row = s.first[lo] + from;
+    x.count = from < all ? min(step, all - from) : 0;
+    x.column0 = 0;
+    x.columns = x.count;
+    x.blocks = lo < a.chunks && x.count ? (a.sum + kPlaces - 1) / kPlaces : 0;
+  }
+  return x;
+}
+
+template <class T, int kForm>
+__global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_constant__ MatmulArgs a) {
+  constexpr bool kWeights = kForm == ZIPCCL_MATMUL_WEIGHTS;
+  constexpr bool kAcrossA = kForm != ZIPCCL_MATMUL_FORWARD, kAcrossB = kWeights;
+  extern __shared__ uint8_t s_raw[];
+  Shared& s = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    tma_prefetch(&a.a);
+    tma_prefetch(&a.b);
+    for (uint32_t i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
+    for (uint32_t i = 0; i < kScaleSets; ++i) mbar_init(&s.scales_full[i], 1), mbar_init(&s.scales_empty[i], 1);
+    mbar_init(&s.clear, 1);
+    mbar_init(&s.cleared, 1);
+    mbar_init(&s.done, 1);
+    mbar_init(&s.taken, 128);
+  }
+  if (warp == 1) tmem_alloc(&s.tmem, 512);
+  after_previous();
+  // the chunks' rows and their tiles
+  for (uint32_t i = threadIdx.x; i < a.chunks; i += kThreads)
+    s.tiles[i] = a.offsets ? (uint32_t)min(max(a.offsets[i + 1], 0), (int32_t)a.rows) : a.rows;
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t end = 0, tiles = 0;
+    for (uint32_t e0 = 0; e0 <= a.chunks; e0 += 32) {  // one more than the chunks: the rows behind them
+      const uint32_t e = e0 + lane;
+      uint32_t top = max(e < a.chunks ? s.tiles[e] : e == a.chunks ? a.rows : 0u, end);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(kAll, top, d);
+        if (lane >= d) top = max(top, y);
+      }
+      uint32_t first = __shfl_up_sync(kAll, top, 1);
+      if (lane == 0) first = end;
+      const uint32_t per = kWeights ? kPlaces : kColumns;
+      const uint32_t n = (top - first + per - 1) / per, upto = tiles + warp_inclusive_sum(n);
+      __syncwarp();
+      if (e <= a.chunks) {
+        s.first[e] = first;
+        s.tiles[e] = upto - n;
+        if (e == a.chunks) s.first[e + 1] = top, s.tiles[e + 1] = upto;
+      }
+      __syncwarp();
+      end = __shfl_sync(kAll, top, 31);
+      tiles = __shfl_sync(kAll, upto, 31);
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = s.tmem;
+  const uint32_t total = kWeights ? a.chunks * a.lane_tiles * a.column_tiles : s.tiles[a.chunks + 1] * a.lane_tiles;
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t n = 0;  // stages filled
+      for (uint32_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const Tile x = tile_of<kWeights>(a, s, t);
+        const uint32_t pieces = kWeights ? (x.columns + kPlaces - 1) / kPlaces : (x.columns + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = kBytesA + pieces * (kWeights ? kPlaces * kPlaces : kBoxRows * kPlaces);
+        for (uint32_t k = 0; k < x.blocks; ++k, ++n) {
+          const uint32_t st = n % kStages;
+          if (!(ok = wait_phase(&s.empty[st], (n / kStages & 1) ^ 1))) break;
+          uint8_t* to = s.stage[st];
+          mbar_arrive_expect_tx(&s.full[st], bytes);
+          const int32_t at = (int32_t)(k * kPlaces);
+          if constexpr (kForm == ZIPCCL_MATMUL_FORWARD) tma_load_3d(to, &a.a, at, x.lane0, x.chunk, &s.full[st]);
+          else if constexpr (kForm == ZIPCCL_MATMUL_BACKWARD) tma_load_3d(to, &a.a, x.lane0, at, x.chunk, &s.full[st]);
+          else tma_load_3d(to, &a.a, x.lane0, x.row + at, 0, &s.full[st]);
+          to += kBytesA;
+          for (uint32_t i = 0; i < pieces; ++i) {
+            if constexpr (kWeights) tma_load_2d(to + i * kPlaces * kPlaces, &a.b, x.column0 + i * kPlaces, x.row + at, &s.full[st]);
+            else tma_load_2d(to + i * kBoxRows * kPlaces, &a.b, at, x.row + i * kBoxRows, &s.full[st]);
+          }
+        }
+      }
+      // a block that gives up does not end under its own copies
+      for (uint32_t i = n > kStages ? n - kStages : 0; !ok && i < n; ++i) wait_phase(&s.full[i % kStages], i / kStages & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t n = 0, sets = 0, tiles = 0, clears = 0;
+      for (uint32_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const Tile x = tile_of<kWeights>(a, s, t);
+        if (x.blocks == 0) continue;
+        if (!(ok = wait_phase(&s.taken, (tiles & 1) ^ 1))) break;
+        tmem_fence_after();
+        const uint32_t word = product_word((x.columns + 31) / 32 * 32, kAcrossA, kAcrossB);
+        uint32_t scales = 0;
+        for (uint32_t k = 0; k < x.blocks; ++k, ++n) {
+          const uint32_t st = n % kStages;
+          if (k % 4 == 0) {
+            const uint32_t set = sets % kScaleSets;
+            if (!(ok = wait_phase(&s.scales_full[set], sets / kScaleSets & 1))) break;
+            tmem_fence_after();
+            scales = tmem + kScaleColumns + sets % 2 * 16;
+            const uint32_t from = smem_addr(s.scales[set]);
+            copy_scales(scales, scale_operand(from));
+            copy_scales(scales + 4, scale_operand(from + 512));
+            if (x.columns > 128) copy_scales(scales + 8, scale_operand(from + 1024));
+            tensor_commit(&s.scales_empty[set]);
+            ++sets;
+          }
+          if (!(ok = wait_phase(&s.full[st], n / kStages & 1))) break;
+          uint32_t steps = 4;
+          if (kWeights && k + 1 == x.blocks && x.count % kPlaces) {
+            steps = (x.count % kPlaces + 31) / 32;
+            if (x.count % 32) {
+              mbar_arrive(&s.clear);
+              if (!(ok = wait_phase(&s.cleared, clears & 1))) break;
+              ++clears;
+            }
+          }
+          tmem_fence_after();
+          const uint32_t at = smem_addr(s.stage[st]);
+          for (uint32_t i = 0; i < steps; ++i)
+            product(tmem, operand(at + i * (kAcrossA ? 4096 : 32), 0), operand(at + kBytesA + i * (kAcrossB ? 4096 : 32), kPlaces * kPlaces),
+                    with_scale(word, k % 4), scales, scales + 4, k + i > 0);
+          tensor_commit(&s.empty[st]);
+        }
+        if (!ok) break;
+        tensor_commit(&s.done);
+        ++tiles;
+      }
+    }
+  } else if (warp == 2) {
+    uint32_t sets = 0;
+    for (uint32_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const Tile x = tile_of<kWeights>(a, s, t);
+      for (uint32_t k0 = 0; k0 < x.blocks; k0 += 4, ++sets) {
+        const uint32_t set = sets % kScaleSets, left = min(4u, x.blocks - k0);
+        // word j of a lane: row 32 j + lane, a byte for each of the four blocks
+        uint32_t w[12];
+#pragma unroll
+        for (int j = 0; j < 12; ++j) w[j] = 0;
+        if constexpr (kWeights) {
+          const uint64_t block = s.tiles[x.chunk] + k0;
+#pragma unroll
+          for (int j = 0; j < 12; ++j) {
+            const uint32_t at = j < 4 ? x.lane0 + 32 * j + lane : x.column0 + 32 * (j - 4) + lane;
+            const uint32_t wide = j < 4 ? a.lanes : a.columns;
+            const uint8_t* p = (j < 4 ? a.scales_a : a.scales_b) + block * wide + at;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i < left && at < wide) w[j] |= (uint32_t)p[(uint64_t)i * wide] << (8 * i);
+          }
+        } else {
+          const uint8_t* p = a.scales_a + x.chunk * a.a_matrix + (uint64_t)(x.lane0 / kLanes) * a.a_lane + (uint64_t)k0 * a.a_block;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < left) w[0] |= (uint32_t)p[(uint64_t)i * a.a_block] << (8 * i);
+          w[1] = w[2] = w[3] = w[0];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t r = 32 * j + lane;
+            const uint8_t* q = a.scales_b + (uint64_t)(x.row + r) * a.b_blocks + k0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i < left && r < x.count) w[4 + j] |= (uint32_t)q[i] << (8 * i);
+          }
+        }
+        if (!(ok = wait_phase(&s.scales_empty[set], (sets / kScaleSets & 1) ^ 1))) break;
+        uint4* to = reinterpret_cast<uint4*>(s.scales[set]) + lane;
+#pragma unroll
+        for (int j = 0; j < 3; ++j) to[32 * j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.scales_full[set]);
+      }
+    }
+  } else if (warp == 3) {
+    if constexpr (kWeights) {
+      uint32_t n = 0, clears = 0;
+      for (uint32_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const Tile x = tile_of<kWeights>(a, s, t);
+        n += x.blocks;
+        if (x.count % 32 == 0) continue;
+        // warp 1 asks for it when the stage has arrived, and goes on when it is done
+        const uint32_t st = (n - 1) % kStages;
+        if (!(ok = wait_phase(&s.clear, clears & 1)) || !(ok = wait_phase(&s.full[st], (n - 1) / kStages & 1))) break;
+        ++clears;
+        const uint32_t from = x.count % kPlaces, upto = (from + 31) / 32 * 32;
+        for (uint32_t i = from * 8 + lane; i < upto * 8; i += 32)
+#pragma unroll
+          for (int piece = 0; piece < 3; ++piece)
+            reinterpret_cast<uint4*>(s.stage[st] + piece * kPlaces * kPlaces)[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.cleared);
+      }
+    }
+  } else {
+    const uint32_t quarter = warp % 4;
+    uint32_t tiles = 0;
+    for (uint32_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const Tile x = tile_of<kWeights>(a, s, t);
+      const uint32_t place = x.lane0 + quarter * 32 + lane;
+      T* out = static_cast<T*>(a.out) + place;
+      if constexpr (kWeights) out += x.chunk * a.out_matrix + x.column0 * a.out_stride;
+      else out += x.row * a.out_stride;
+      if (x.blocks) {
+        if (!(ok = wait_phase(&s.done, tiles & 1))) break;
+        tmem_fence_after();
+      }
+      for (uint32_t c = 0; c < x.columns; c += 32) {
+        uint32_t v[32];
+        if (x.blocks) {
+          tmem_load32(tmem + (quarter << 21) + c, v);
+          tmem_wait_load();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0;
+        }
+        if (place < a.lanes) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < x.columns) out[(c + i) * a.out_stride] = from_float<T>(__uint_as_float(v[i]));
+        }
+      }
+      if (x.blocks) {
+        tmem_fence_before();
+        mbar_arrive(&s.taken);
+        ++tiles;
+      }
+    }
+  }
+  if (!ok) atomicOr(&g_wait_ran_out, 1u);
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- host
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+Encode encoder() {
+  static std::atomic<void*> found{nullptr};
+  void* f = found.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      return nullptr;
+    found.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<Encode>(f);
+}
+
+// Map of codes [matrices][rows][cols]; a copy takes 128 bytes of `box` rows.  Rows
+// and columns beyond the matrix read as zeros.
+bool code_map(CUtensorMap* m, const zipccl_fp8_blocks* x, uint64_t cols, uint64_t rows, uint64_t matrices, uint32_t dims,
+              uint32_t box) {
+  const Encode f = encoder();
+  const cuuint64_t size[3] = {cols, rows, matrices}, strides[2] = {x->stride, x->stride * rows};
+  const cuuint32_t boxes[3] = {kPlaces, box, 1}, steps[3] = {1, 1, 1};
+  return f && f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, const_cast<uint8_t*>(x->d_codes), size, strides, boxes, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t kSmem = sizeof(Shared) + 1024;
+
+template <class T, int kForm>
+cudaError_t matmul_launch(const MatmulArgs& a, uint64_t tiles, cudaStream_t s) {
+  static std::atomic<int> multiprocessors[kMaxDevices];
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!(sms = multiprocessors[dev].load(std::memory_order_acquire))) {
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(zc_matmul_kernel<T, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem)) != cudaSuccess)
+      return e;
+    multiprocessors[dev].store(sms, std::memory_order_release);
+  }
+  return launch(zc_matmul_kernel<T, kForm>, (uint32_t)std::min<uint64_t>(tiles, sms), kThreads, kSmem, s, a);
+}
+
+template <class T>
+cudaError_t matmul_by_form(const MatmulArgs& a, int form, uint64_t tiles, cudaStream_t s) {
+  return form == ZIPCCL_MATMUL_FORWARD    ? matmul_launch<T, ZIPCCL_MATMUL_FORWARD>(a, tiles, s)
+         : form == ZIPCCL_MATMUL_BACKWARD ? matmul_launch<T, ZIPCCL_MATMUL_BACKWARD>(a, tiles, s)
+                                          : matmul_launch<T, ZIPCCL_MATMUL_WEIGHTS>(a, tiles, s);
+}
+
+bool good(const zipccl_fp8_blocks* x, uint64_t cols) {
+  return x->d_codes && x->d_scales && host_aligned(x->d_codes, 16) && x->stride >= cols && x->stride % 16 == 0 && x->stride < (1ull << 38);
+}
+
+}  // namespace
+}  // namespace zc
+
+using namespace zc;
+
+extern "C" {
+
+zipccl_status zipccl_moe_matmul(int form, const zipccl_fp8_blocks* a, const zipccl_fp8_blocks* b, uint64_t rows,
+                                uint64_t inner, uint64_t outer, const int32_t* d_offsets, uint32_t experts, void* d_out,
+                                int out_type, uint64_t out_stride, void* stream) {
+  const uint64_t z = type_bytes(out_type), kMaxCols = 1ull << 22;
+  const bool weights = form == ZIPCCL_MATMUL_WEIGHTS;
+  if (form < ZIPCCL_MATMUL_FORWARD || form > ZIPCCL_MATMUL_WEIGHTS || z == 0 || !a || !b) return ZIPCCL_ERR_INVALID_ARG;
+  if (rows >= (1ull << 31) || inner == 0 || outer == 0 || inner > kMaxCols || outer > kMaxCols || experts == 0 ||
+      experts > kMaxChunks || (!d_offsets && experts != 1) || !host_aligned(d_offsets, 4))
+    return ZIPCCL_ERR_INVALID_ARG;
+  const uint64_t out_cols = form == ZIPCCL_MATMUL_FORWARD ? outer : inner;
+  if (out_stride < out_cols || out_stride >= (1ull << 32)) return ZIPCCL_ERR_INVALID_ARG;
+  if (rows == 0 && !weights) return ZIPCCL_OK;
+  if (!d_out || !host_aligned(d_out, z)) return ZIPCCL_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0)
+    return cudaMemset2DAsync(d_out, out_stride * z, 0, inner * z, (size_t)experts * outer, s) == cudaSuccess ? ZIPCCL_OK : ZIPCCL_ERR_CUDA;
+  if (!good(a, form == ZIPCCL_MATMUL_FORWARD ? inner : outer) || !good(b, inner)) return ZIPCCL_ERR_INVALID_ARG;
+  MatmulArgs m{};
+  m.offsets = d_offsets;
+  m.out = d_out;
+  m.out_stride = out_stride;
+  m.out_matrix = out_stride * outer;
+  m.rows = (uint32_t)rows;
+  m.chunks = experts;
+  m.lanes = (uint32_t)out_cols;
+  m.lane_tiles = (m.lanes + kLanes - 1) / kLanes;
+  uint64_t tiles;
+  bool mapped;
+  if (weights) {
+    m.scales_a = b->d_scales;
+    m.scales_b = a->d_scales;
+    m.columns = (uint32_t)outer;
+    m.column_tiles = (m.columns + kColumns - 1) / kColumns;
+    mapped = code_map(&m.a, b, inner, rows, 1, 3, kPlaces) && code_map(&m.b, a, outer, rows, 1, 2, kPlaces);
+    tiles = (uint64_t)experts * m.lane_tiles * m.column_tiles;
+  } else {
+    const uint32_t high = (uint32_t)((outer + kFp8Block - 1) / kFp8Block), wide = (uint32_t)((inner + kFp8Block - 1) / kFp8Block);
+    const bool forward = form == ZIPCCL_MATMUL_FORWARD;
+    m.scales_a = b->d_scales;
+    m.scales_b = a->d_scales;
+    m.a_matrix = (uint64_t)high * wide;
+    m.a_lane = forward ? wide : 1;
+    m.a_block = forward ? 1 : wide;
+    m.sum = (uint32_t)(forward ? inner : outer);
+    m.b_blocks = forward ? wide : high;
+    mapped = code_map(&m.a, b, inner, outer, experts, 3, kPlaces) && code_map(&m.b, a, m.sum, rows, 1, 2, kBoxRows);
+    tiles = (rows / kColumns + experts + 1) * m.lane_tiles;  // at most
+  }
+  if (!mapped) return ZIPCCL_ERR_CUDA;
+  if (tiles >= (1ull << 32)) return ZIPCCL_ERR_INVALID_ARG;
+  const cudaError_t e = out_type == ZIPCCL_TYPE_F32    ? matmul_by_form<float>(m, form, tiles, s)
+                        : out_type == ZIPCCL_TYPE_BF16 ? matmul_by_form<__nv_bfloat16>(m, form, tiles, s)
+                                                       : matmul_by_form<__half>(m, form, tiles, s);
+  return e == cudaSuccess ? ZIPCCL_OK : ZIPCCL_ERR_CUDA;
+}
+
+zipccl_status zipccl_moe_status(void* stream) {
+  unsigned int v = 0, zero = 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaMemcpyFromSymbolAsync(&v, g_wait_ran_out, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return ZIPCCL_ERR_CUDA;
+  if (!v) return ZIPCCL_OK;
+  if (cudaMemcpyToSymbolAsync(g_wait_ran_out, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return ZIPCCL_ERR_CUDA;
+  return ZIPCCL_ERR_TIMEOUT;
+}
+
+}  // extern "C"

@@ -1,0 +1,111 @@
+// zc_tensor.cuh -- the tensor cores' pieces: matrices read tile by tile through
+// tensor maps, block-scaled 8-bit products with sums in tensor memory, waits
+// with an end.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "zc_device.cuh"
+
+namespace zc {
+
+// Waits for phase `parity`; false after kWaitLimitNs.  The clock is read only
+// where the phase is not complete at once.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done ? true : mbar_wait(bar, parity);
+}
+
+// ---- tensor maps
+__device__ __forceinline__ void tma_prefetch(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(void* dst, const void* map, int32_t x, int32_t y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int32_t x, int32_t y, int32_t z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// ---- tensor memory: 128 lanes x 512 columns of 32 bits
+__device__ __forceinline__ void tmem_alloc(uint32_t* at, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(columns) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// 32 columns of the warp's 32 lanes: a lane's values of 32 consecutive columns.
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]),
+        "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]),
+        "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(at)
+      : "memory");
+}
+
+// Arrives once on `bar` when the tensor operations that this thread has issued are done.
+__device__ __forceinline__ void tensor_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Descriptor of an operand in shared memory: lines of 128 bytes, their 16-byte
+// pieces exchanged as a 128-byte swizzled tensor copy leaves them, 8 lines to
+// the next 1,024 bytes.  Along the sum: a line holds 128 places of the sum (an
+// instruction takes 32, a quarter line further each).  Across it: a line holds
+// one place of the sum for 128 rows of the operand, `apart` bytes to the next
+// 128 rows (an instruction takes 32 lines).
+__device__ __forceinline__ uint64_t operand(uint32_t smem, uint32_t apart) {
+  return (uint64_t)((smem & 0x3FFFFu) >> 4) | (uint64_t)(apart >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// The same for scales: 512 bytes, plain.
+__device__ __forceinline__ uint64_t scale_operand(uint32_t smem) {
+  return (uint64_t)((smem & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | 1ull << 46;
+}
+
+// 128 rows' scales into four columns of tensor memory: 32 lanes x 16 bytes, for
+// each of the four quarters of its lanes.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t from) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(from) : "memory");
+}
+
+// Instruction word of an E4M3 x E4M3 product of 128 x `columns`, E8M0 scales;
+// mn_a, mn_b: the operand lies across the sum.
+__device__ __forceinline__ uint32_t product_word(uint32_t columns, bool mn_a, bool mn_b) {
+  return (uint32_t)mn_a << 15 | (uint32_t)mn_b << 16 | (columns >> 3) << 17 | 1u << 23 | 1u << 27;
+}
+// The same with byte `i` of the scales' words.
+__device__ __forceinline__ uint32_t with_scale(uint32_t word, uint32_t i) { return word | i << 4 | i << 29; }
+
+// 32 places of the sum: tensor memory at d (+)= a x b.
+__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t word, uint32_t scale_a, uint32_t scale_b,
+                                        bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(word), "r"(scale_a), "r"(scale_b), "r"((uint32_t)add)
+      : "memory");
+}
+
+}  // namespace zc

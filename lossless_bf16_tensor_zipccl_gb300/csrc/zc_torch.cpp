@@ -445,10 +445,200 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ---- 8-bit blocks: a pair (codes, scales)
+uint8_t* bytes(const Tensor& t) { return static_cast<uint8_t*>(t.data_ptr()); }
+
+struct Blocks {
+  Tensor codes, scales;
+};
+
+// (codes, scales) of an argument.
+Blocks blocks(PyObject* o, const char* what) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 2) refuse(PyExc_TypeError, "%s: expected Fp8Blocks (codes, scales)", what);
+  Blocks b{tensor(PyTuple_GET_ITEM(o, 0), what), tensor(PyTuple_GET_ITEM(o, 1), what)};
+  if (b.codes.scalar_type() != ScalarType::Float8_e4m3fn)
+    refuse(PyExc_TypeError, "%s: expected codes of Float8_e4m3fn, got %s", what, toString(b.codes.scalar_type()));
+  if (b.scales.scalar_type() != ScalarType::Float8_e8m0fnu)
+    refuse(PyExc_TypeError, "%s: expected scales of Float8_e8m0fnu, got %s", what, toString(b.scales.scalar_type()));
+  return b;
+}
+
+// Bytes between rows of codes [.., rows, cols], whose matrices lie rows apart.
+uint64_t code_stride(const Tensor& t, const char* what) {
+  const int64_t d = t.dim(), rows = t.size(d - 2), cols = t.size(d - 1);
+  const bool apart = rows > 1 || (d == 3 && t.size(0) > 1);
+  const int64_t stride = rows > 1 ? t.stride(d - 2) : d == 3 && t.size(0) > 1 ? t.stride(0) : (cols + 15) / 16 * 16;
+  if (!t.is_cuda() || (cols > 1 && t.stride(d - 1) != 1) || (apart && (stride % 16 || stride < cols)) ||
+      (d == 3 && t.size(0) > 1 && t.stride(0) != stride * rows))
+    refuse(PyExc_ValueError, "%s: expected CUDA codes whose rows are contiguous and a multiple of 16 bytes apart", what);
+  return (uint64_t)stride;
+}
+
+int64_t block_count(int64_t n) { return (n + ZIPCCL_FP8_BLOCK - 1) / ZIPCCL_FP8_BLOCK; }
+
+// Blocks that a call fills: given, or allocated with rows of a multiple of 16 bytes.
+Blocks new_blocks(const Call& call, PyObject* o, IntArrayRef shape, IntArrayRef scale_shape, const char* what) {
+  if (o != Py_None) {
+    Blocks b = blocks(o, what);
+    if (b.codes.sizes() != shape) refuse(PyExc_ValueError, "%s: codes of another shape were expected", what);
+    if (b.codes.device() != call.device) refuse(PyExc_ValueError, "%s: expected tensors on the device of the call's others", what);
+    plain(b.scales, ScalarType::Float8_e8m0fnu, scale_shape, call.device, what);
+    code_stride(b.codes, what);
+    written(b.codes);
+    written(b.scales);
+    return b;
+  }
+  std::vector<int64_t> held(shape.begin(), shape.end());
+  const int64_t cols = held.back();
+  held.back() = (cols + 15) / 16 * 16;
+  Tensor codes = call.empty(held, ScalarType::Float8_e4m3fn);
+  if (held.back() != cols) codes = codes.slice(-1, 0, cols);
+  return {codes, call.empty(scale_shape, ScalarType::Float8_e8m0fnu)};
+}
+
+PyObject* pair(const Blocks& b) {
+  PyObject* both = PyTuple_New(2);
+  if (!both) throw python_error();
+  PyTuple_SET_ITEM(both, 0, THPVariable_Wrap(b.codes));
+  PyTuple_SET_ITEM(both, 1, THPVariable_Wrap(b.scales));
+  return both;
+}
+
+// Offsets of the chunks (None: one chunk) and how many chunks there are.
+const int32_t* chunk_offsets(PyObject* o, c10::Device device, int64_t* experts) {
+  *experts = 1;
+  if (o == Py_None) return nullptr;
+  const Tensor& t = tensor(o, "offsets");
+  if (t.dim() != 1 || t.numel() < 2) refuse(PyExc_ValueError, "offsets: expected one dimension, one value more than there are experts");
+  *experts = t.numel() - 1;
+  return static_cast<const int32_t*>(plain(t, ScalarType::Int, t.sizes(), device, "offsets").const_data_ptr());
+}
+
+bool bad_chunks(int64_t experts) { return experts > 1024; }
+bool bad_widths(int64_t a, int64_t b = 1) { return a > 1 << 22 || b > 1 << 22; }
+
+// rows, out, stream
+PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 3);
+  no_autograd("moe_quantize", {a[0]});
+  const Tensor& x = tensor(a[0], "rows");
+  const int type = value_type(x, "rows");
+  const uint64_t stride = row_stride(x, "rows");
+  const int64_t rows = x.size(0), cols = x.size(1);
+  if (bad_widths(cols)) return refused();
+  const Call call(x.device(), a[2]);
+  const Blocks b = new_blocks(call, a[1], {rows, cols}, {rows, block_count(cols)}, "out");
+  const zipccl_status st = zipccl_moe_quantize(x.const_data_ptr(), type, stride, rows, cols, bytes(b.codes), code_stride(b.codes, "out"),
+                                               bytes(b.scales), call.stream);
+  return st == ZIPCCL_OK ? pair(b) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// rows, offsets, by_rows, out, rows_out, stream
+PyObject* quantize_columns(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 6);
+  no_autograd("moe_quantize_columns", {a[0]});
+  const Tensor& x = tensor(a[0], "rows");
+  const int type = value_type(x, "rows");
+  const uint64_t stride = row_stride(x, "rows");
+  const int64_t rows = x.size(0), cols = x.size(1);
+  int64_t experts;
+  const int32_t* offsets = chunk_offsets(a[1], x.device(), &experts);
+  if (bad_widths(cols) || bad_chunks(experts)) return refused();
+  const bool both = PyObject_IsTrue(a[2]) == 1;
+  if (!both && a[4] != Py_None) refuse(PyExc_ValueError, "rows_out is given and by_rows is not");
+  const Call call(x.device(), a[5]);
+  const Blocks b = new_blocks(call, a[3], {rows, cols}, {rows / (int64_t)ZIPCCL_FP8_BLOCK + experts, cols}, "out");
+  Blocks r;
+  if (both) r = new_blocks(call, a[4], {rows, cols}, {rows, block_count(cols)}, "rows_out");
+  const zipccl_status st = zipccl_moe_quantize_columns(
+      x.const_data_ptr(), type, stride, rows, cols, offsets, (uint32_t)experts, bytes(b.codes), code_stride(b.codes, "out"),
+      bytes(b.scales), both ? bytes(r.codes) : nullptr, both ? code_stride(r.codes, "rows_out") : 0, both ? bytes(r.scales) : nullptr,
+      call.stream);
+  if (st != ZIPCCL_OK) return PyLong_FromLong(st);
+  if (!both) return pair(b);
+  PyObject* out = PyTuple_New(2);
+  if (!out) throw python_error();
+  PyTuple_SET_ITEM(out, 0, pair(r));
+  PyTuple_SET_ITEM(out, 1, pair(b));
+  return out;
+  END_HANDLE_TH_ERRORS
+}
+
+// weights, out, stream
+PyObject* quantize_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 3);
+  no_autograd("moe_quantize_weights", {a[0]});
+  const Tensor& w = tensor(a[0], "weights");
+  const int type = value_type(w, "weights");
+  if (w.dim() != 2 && w.dim() != 3) refuse(PyExc_ValueError, "weights: expected two or three dimensions");
+  plain(w, w.scalar_type(), w.sizes(), cuda_device(w, "weights"), "weights");
+  const int64_t experts = w.dim() == 3 ? w.size(0) : 1, rows = w.size(-2), cols = w.size(-1);
+  if (bad_widths(rows, cols) || bad_chunks(experts)) return refused();
+  const Call call(w.device(), a[2]);
+  std::vector<int64_t> scales = {block_count(rows), block_count(cols)};
+  if (w.dim() == 3) scales.insert(scales.begin(), experts);
+  const Blocks b = new_blocks(call, a[1], w.sizes(), scales, "out");
+  const zipccl_status st = zipccl_moe_quantize_weights(w.const_data_ptr(), type, (uint32_t)experts, rows, cols, bytes(b.codes),
+                                                       code_stride(b.codes, "out"), bytes(b.scales), call.stream);
+  return st == ZIPCCL_OK ? pair(b) : PyLong_FromLong(st);
+  END_HANDLE_TH_ERRORS
+}
+
+// form, a, b, offsets, type, out, stream
+PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 7);
+  const int form = (int)integer(a[0]);
+  const bool by_weights = form == ZIPCCL_MATMUL_WEIGHTS, forward = form == ZIPCCL_MATMUL_FORWARD;
+  const char* names[2] = {forward ? "rows" : by_weights ? "grad_columns" : "grad_rows", by_weights ? "columns" : "weights"};
+  const Blocks x = blocks(a[1], names[0]), w = blocks(a[2], names[1]);
+  const c10::Device device = cuda_device(x.codes, names[0]);
+  int64_t experts;
+  const int32_t* offsets = chunk_offsets(a[3], device, &experts);
+  two_dims(x.codes, names[0]);
+  if (by_weights) two_dims(w.codes, names[1]);
+  else if (w.codes.dim() != (offsets ? 3 : 2))
+    refuse(PyExc_ValueError, "%s: expected %s dimensions", names[1], offsets ? "three" : "two");
+  const int64_t rows = x.codes.size(0), inner = w.codes.size(-1), outer = by_weights ? x.codes.size(1) : w.codes.size(-2);
+  if (!by_weights && offsets && w.codes.size(0) != experts) refuse(PyExc_ValueError, "%s: a matrix for each chunk was expected", names[1]);
+  if (by_weights ? w.codes.size(0) != rows : x.codes.size(1) != (forward ? inner : outer))
+    refuse(PyExc_ValueError, "%s and %s: sizes that fit each other were expected", names[0], names[1]);
+  if (bad_widths(inner, outer) || bad_chunks(experts)) return refused();
+  if (w.codes.device() != device) refuse(PyExc_ValueError, "%s: expected a tensor on the device of the call's others", names[1]);
+  constexpr ScalarType scale = ScalarType::Float8_e8m0fnu;
+  if (by_weights) {
+    const int64_t blocks = rows / (int64_t)ZIPCCL_FP8_BLOCK + experts;
+    plain(x.scales, scale, {blocks, outer}, device, names[0]);
+    plain(w.scales, scale, {blocks, inner}, device, names[1]);
+  } else {
+    plain(x.scales, scale, {rows, block_count(x.codes.size(1))}, device, names[0]);
+    if (offsets) plain(w.scales, scale, {experts, block_count(outer), block_count(inner)}, device, names[1]);
+    else plain(w.scales, scale, {block_count(outer), block_count(inner)}, device, names[1]);
+  }
+  const int type = (int)integer(a[4]);
+  const ScalarType to = type == ZIPCCL_TYPE_F32 ? ScalarType::Float : type == ZIPCCL_TYPE_BF16 ? ScalarType::BFloat16 : ScalarType::Half;
+  const zipccl_fp8_blocks xa = {bytes(x.codes), bytes(x.scales), code_stride(x.codes, names[0])};
+  const zipccl_fp8_blocks wb = {bytes(w.codes), bytes(w.scales), code_stride(w.codes, names[1])};
+  const Call call(device, a[6]);
+  std::vector<int64_t> shape = by_weights ? std::vector<int64_t>{outer, inner} : std::vector<int64_t>{rows, forward ? outer : inner};
+  if (by_weights && offsets) shape.insert(shape.begin(), experts);
+  const Tensor out = call.result(a[5], shape, to, "out");
+  return answer(zipccl_moe_matmul(form, &xa, &wb, rows, inner, outer, offsets, (uint32_t)experts, out.data_ptr(), type, shape.back(),
+                                  call.stream),
+                {out});
+  END_HANDLE_TH_ERRORS
+}
+
 #define ZC_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ZC_METHOD(route),             ZC_METHOD(route_backward), ZC_METHOD(plan),
                          ZC_METHOD(dispatch),          ZC_METHOD(dispatch_backward), ZC_METHOD(combine),
-                         ZC_METHOD(combine_backward),  ZC_METHOD(adamw),          {nullptr, nullptr, 0, nullptr}};
+                         ZC_METHOD(combine_backward),  ZC_METHOD(adamw),          ZC_METHOD(quantize),
+                         ZC_METHOD(quantize_columns),  ZC_METHOD(quantize_weights), ZC_METHOD(matmul),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_zipccl_torch", "Operator calls of libzipccl on torch tensors.", -1, methods};
 
 }  // namespace

@@ -28,12 +28,17 @@ import torch
 from . import _build, _check, load
 
 __all__ = ["ADAMW_BLOCK", "MoePlan", "moe_route", "moe_route_backward", "moe_plan", "moe_dispatch",
-           "moe_dispatch_backward", "moe_combine", "moe_combine_backward", "adamw_step", "adamw_state"]
+           "moe_dispatch_backward", "moe_combine", "moe_combine_backward", "adamw_step", "adamw_state", "FP8_BLOCK",
+           "Fp8Blocks", "moe_quantize", "moe_quantize_columns", "moe_quantize_weights", "moe_matmul",
+           "moe_matmul_backward", "moe_matmul_backward_weights", "moe_status"]
 
 ADAMW_BLOCK = 256  # values that share one scale of an 8-bit state
+FP8_BLOCK = 128    # values, rows or both that share one scale of 8-bit operands
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _GROUP_SCORES = {"max": 0, "top2": 1}
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_FORWARD, _BACKWARD, _WEIGHTS = range(3)
 
 
 def _load_native():
@@ -55,6 +60,14 @@ class MoePlan(NamedTuple):
     counts: torch.Tensor
     offsets: torch.Tensor
     slots: torch.Tensor
+
+
+class Fp8Blocks(NamedTuple):
+    """8-bit values: codes (float8_e4m3fn, rows a multiple of 16 bytes apart)
+    times a power of two for each block of 128 (scales, float8_e8m0fnu,
+    contiguous)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
 
 
 def _choice(options, name, value):
@@ -131,6 +144,67 @@ def moe_combine_backward(grad_out, rows, slots, weights=None, *, grad_rows=None,
     gradient is grad_out itself."""
     return _done(_native.combine_backward(grad_out, rows, slots, weights, grad_rows, grad_weights, _handle(stream)),
                  "zipccl_moe_combine_backward")
+
+
+def moe_quantize(rows, *, out=None, stream=None) -> Fp8Blocks:
+    """rows [n, cols] in 8 bits, blocks of 128 values along a row (see
+    zipccl_moe_quantize): codes [n, cols], scales [n, ceil(cols / 128)].  Rows
+    may have any stride.  The operand of ``moe_matmul`` and, for gradients, of
+    ``moe_matmul_backward``."""
+    return Fp8Blocks(*_done(_native.quantize(rows, out, _handle(stream)), "zipccl_moe_quantize"))
+
+
+def moe_quantize_columns(rows, offsets=None, *, by_rows: bool = False, out=None, rows_out=None, stream=None):
+    """rows [n, cols] in 8 bits, blocks of 128 rows of a chunk down a column:
+    codes [n, cols], scales [n // 128 + experts, cols].  ``offsets`` is
+    ``plan.offsets`` (None: all rows are one chunk).  With ``by_rows`` what
+    ``moe_quantize`` gives too, from the same reading: (by rows, by columns).
+    Both operands of ``moe_matmul_backward_weights``."""
+    made = _done(_native.quantize_columns(rows, offsets, by_rows, out, rows_out, _handle(stream)),
+                 "zipccl_moe_quantize_columns")
+    return (Fp8Blocks(*made[0]), Fp8Blocks(*made[1])) if by_rows else Fp8Blocks(*made)
+
+
+def moe_quantize_weights(weights, *, out=None, stream=None) -> Fp8Blocks:
+    """The experts' matrices [experts, outer, inner] (or one, [outer, inner]) in
+    8 bits, blocks of 128 x 128: forward and backward read the same codes."""
+    return Fp8Blocks(*_done(_native.quantize_weights(weights, out, _handle(stream)), "zipccl_moe_quantize_weights"))
+
+
+def _matmul(form, a, b, offsets, dtype, out, stream):
+    try:
+        type_ = _TYPES[dtype]
+    except KeyError:
+        raise TypeError(f"dtype: expected float32, bfloat16 or float16, got {dtype}") from None
+    return _done(_native.matmul(form, a, b, offsets, type_, out, _handle(stream)), "zipccl_moe_matmul")
+
+
+def moe_matmul(rows, weights, offsets=None, *, dtype=torch.bfloat16, out=None, stream=None):
+    """Every row times its expert's matrix: out[m] = weights[e] @ rows[m] for the
+    rows of chunk e, [n, outer]; rows behind the last chunk become zeros.
+    ``rows`` from ``moe_quantize``, ``weights`` from ``moe_quantize_weights``;
+    without ``offsets`` one matrix [outer, inner] for all rows."""
+    return _matmul(_FORWARD, rows, weights, offsets, dtype, out, stream)
+
+
+def moe_matmul_backward(grad_rows, weights, offsets=None, *, dtype=torch.bfloat16, out=None, stream=None):
+    """Gradient of ``moe_matmul`` by the rows, [n, inner], from the result's
+    gradient in 8 bits by rows (``moe_quantize``)."""
+    return _matmul(_BACKWARD, grad_rows, weights, offsets, dtype, out, stream)
+
+
+def moe_matmul_backward_weights(grad_columns, columns, offsets=None, *, dtype=torch.bfloat16, out=None, stream=None):
+    """Gradient of ``moe_matmul`` by the weights, [experts, outer, inner] (one
+    matrix without ``offsets``), from the result's gradient and the rows, both
+    by columns of the same chunks (``moe_quantize_columns``)."""
+    return _matmul(_WEIGHTS, grad_columns, columns, offsets, dtype, out, stream)
+
+
+def moe_status(stream=None) -> None:
+    """Raises ``ZipcclError`` if a wait inside a ``moe_matmul`` call on the
+    current device has run out since the last such call (synchronizes)."""
+    handle = torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+    _check(load().zipccl_moe_status(handle), "zipccl_moe_status")
 
 
 def adamw_state(param, bits: int = 32):

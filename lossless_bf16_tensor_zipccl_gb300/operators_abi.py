@@ -1,5 +1,5 @@
 """The operator calls of ``include/zipccl.h`` (routing, plan, dispatch, combine,
-AdamW step): records, argument types and pointer-level mirrors, without torch.
+AdamW step, 8-bit blocks and their products): records, argument types and pointer-level mirrors, without torch.
 ``operators`` has the same calls on tensors."""
 from __future__ import annotations
 
@@ -11,10 +11,13 @@ __all__ = [
     "TYPE_F32", "TYPE_BF16", "TYPE_F16", "RouteOptions", "AdamWTensor", "AdamWOptions",
     "zipccl_moe_route", "zipccl_moe_route_backward", "zipccl_moe_plan_workspace_bytes", "zipccl_moe_plan",
     "zipccl_moe_dispatch", "zipccl_moe_dispatch_backward", "zipccl_moe_combine", "zipccl_moe_combine_backward",
-    "zipccl_adamw_step",
+    "zipccl_adamw_step", "MATMUL_FORWARD", "MATMUL_BACKWARD", "MATMUL_WEIGHTS", "Fp8BlocksArg",
+    "zipccl_moe_quantize", "zipccl_moe_quantize_columns", "zipccl_moe_quantize_weights", "zipccl_moe_matmul",
+    "zipccl_moe_status",
 ]
 
 TYPE_F32, TYPE_BF16, TYPE_F16 = range(3)
+MATMUL_FORWARD, MATMUL_BACKWARD, MATMUL_WEIGHTS = range(3)
 
 
 class RouteOptions(ctypes.Structure):
@@ -34,6 +37,10 @@ class AdamWOptions(ctypes.Structure):
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_uint64)]
 
 
+class Fp8BlocksArg(ctypes.Structure):
+    _fields_ = [("d_codes", ctypes.c_void_p), ("d_scales", ctypes.c_void_p), ("stride", ctypes.c_uint64)]
+
+
 def declare(L) -> None:
     """Argument types of the library's operator calls (used by ``load``)."""
     u64, u32, i32, vp = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int, ctypes.c_void_p
@@ -48,9 +55,17 @@ def declare(L) -> None:
     L.zipccl_moe_combine_backward.argtypes = [vp, vp, i32, u64, u32, u64, vp, vp, vp, vp, vp]
     L.zipccl_adamw_step.argtypes = [ctypes.POINTER(AdamWTensor), u32, i32, i32, i32, ctypes.POINTER(AdamWOptions),
                                     vp, vp]
+    L.zipccl_moe_quantize.argtypes = [vp, i32, u64, u64, u64, vp, u64, vp, vp]
+    L.zipccl_moe_quantize_columns.argtypes = [vp, i32, u64, u64, u64, vp, u32, vp, u64, vp, vp, u64, vp, vp]
+    L.zipccl_moe_quantize_weights.argtypes = [vp, i32, u32, u64, u64, vp, u64, vp, vp]
+    blocks = ctypes.POINTER(Fp8BlocksArg)
+    L.zipccl_moe_matmul.argtypes = [i32, blocks, blocks, u64, u64, u64, vp, u32, vp, i32, u64, vp]
+    L.zipccl_moe_status.argtypes = [vp]
     for name in ("zipccl_moe_route", "zipccl_moe_route_backward", "zipccl_moe_plan_workspace_bytes",
                  "zipccl_moe_plan", "zipccl_moe_dispatch", "zipccl_moe_dispatch_backward", "zipccl_moe_combine",
-                 "zipccl_moe_combine_backward", "zipccl_adamw_step"):
+                 "zipccl_moe_combine_backward", "zipccl_adamw_step",
+                 "zipccl_moe_quantize", "zipccl_moe_quantize_columns", "zipccl_moe_quantize_weights",
+                 "zipccl_moe_matmul", "zipccl_moe_status"):
         getattr(L, name).restype = ctypes.c_int
 
 
@@ -107,3 +122,31 @@ def zipccl_adamw_step(tensors, n_tensors: int, param_type: int, grad_type: int, 
     """tensors: a ctypes array of at least n_tensors AdamWTensor records."""
     return load().zipccl_adamw_step(tensors, n_tensors, param_type, grad_type, state_bits, options, d_grad_scale,
                                     stream)
+
+
+def zipccl_moe_quantize(d_x: int, type: int, row_stride: int, rows: int, cols: int, d_codes: int, code_stride: int,
+                        d_scales: int, stream: int) -> int:
+    return load().zipccl_moe_quantize(d_x, type, row_stride, rows, cols, d_codes, code_stride, d_scales, stream)
+
+
+def zipccl_moe_quantize_columns(d_x: int, type: int, row_stride: int, rows: int, cols: int, d_offsets: int,
+                                experts: int, d_codes: int, code_stride: int, d_scales: int, d_row_codes: int,
+                                row_code_stride: int, d_row_scales: int, stream: int) -> int:
+    return load().zipccl_moe_quantize_columns(d_x, type, row_stride, rows, cols, d_offsets, experts, d_codes,
+                                              code_stride, d_scales, d_row_codes, row_code_stride, d_row_scales,
+                                              stream)
+
+
+def zipccl_moe_quantize_weights(d_w: int, type: int, experts: int, rows: int, cols: int, d_codes: int,
+                                code_stride: int, d_scales: int, stream: int) -> int:
+    return load().zipccl_moe_quantize_weights(d_w, type, experts, rows, cols, d_codes, code_stride, d_scales, stream)
+
+
+def zipccl_moe_matmul(form: int, a: Fp8BlocksArg, b: Fp8BlocksArg, rows: int, inner: int, outer: int, d_offsets: int,
+                      experts: int, d_out: int, out_type: int, out_stride: int, stream: int) -> int:
+    return load().zipccl_moe_matmul(form, a, b, rows, inner, outer, d_offsets, experts, d_out, out_type, out_stride,
+                                    stream)
+
+
+def zipccl_moe_status(stream: int) -> int:
+    return load().zipccl_moe_status(stream)
