@@ -541,6 +541,51 @@ zipccl_status zipccl_moe_matmul(int form, const zipccl_fp8_blocks *a, const zipc
                                 uint32_t experts, void *d_out, int out_type, uint64_t out_stride, void *stream);
 zipccl_status zipccl_moe_status(void *stream);
 
+/*
+ * A whole mixture-of-experts layer for up to ZIPCCL_LAYER_MAX_TOKENS tokens, in
+ * two kernels.  With x a token's row:
+ *   logits = router x, in 32 bits; weights and ids as zipccl_moe_route gives for
+ *     them (options, d_bias, d_mask: the same)
+ *   h_k    = act(gate x) * (up x), where gate and up are the first and the last
+ *     `inner` rows of expert k's matrix in d_up; ungated: act(up x)
+ *   y      = d_residual + sum over the token's experts of weight_k * down_k h_k
+ * Sums and h are held in 32 bits; a 32-bit operand takes part with 21 bits at
+ * least (two parts of 11), a 16- or 8-bit one exactly.  A token without experts
+ * gets its residual, or 0.  A result that something infinite or NaN takes part in
+ * is infinite or NaN.
+ *   d_x [tokens][hidden] of `type`, rows x_stride values apart; d_router
+ *     [experts][hidden] of router_type: `type` or F32; d_up [experts]
+ *     [gated ? 2 inner : inner][hidden], d_down [experts][hidden][inner]: of
+ *     `type` (weight_bits those of the type), or 8-bit blocks (weight_bits 8,
+ *     scales as zipccl_moe_quantize_weights leaves them); rows up_stride and
+ *     down_stride values apart;
+ *     d_residual, d_y [tokens][hidden], d_residual may be d_y;
+ *     d_weights, d_ids [tokens][top_k], written.
+ * act: SILU v / (1 + exp(-v)); GELU v (1 + erf(v / sqrt 2)) / 2; RELU max(v, 0).
+ * d_ws: 256-byte aligned, zipccl_moe_layer_workspace_bytes bytes; nothing in it
+ * has to be set, and nothing is kept in it.
+ */
+#define ZIPCCL_LAYER_MAX_TOKENS 32u
+typedef enum { ZIPCCL_ACTIVATION_SILU = 0, ZIPCCL_ACTIVATION_GELU = 1, ZIPCCL_ACTIVATION_RELU = 2 } zipccl_activation;
+
+typedef struct {
+    const void *d_x, *d_router, *d_up, *d_down;
+    const void *d_residual;                      /* nullable */
+    const uint8_t *d_up_scales, *d_down_scales;  /* weight_bits 8 only */
+    const float *d_bias;                         /* nullable */
+    const uint8_t *d_mask;                       /* nullable */
+    void *d_y;
+    float *d_weights;
+    int32_t *d_ids;
+    uint64_t tokens, hidden, inner, x_stride, up_stride, down_stride;
+    uint32_t experts;
+    int32_t type, router_type, weight_bits, gated, activation;
+} zipccl_moe_layer_args;
+
+zipccl_status zipccl_moe_layer_workspace_bytes(uint64_t tokens, uint32_t top_k, uint64_t inner, uint64_t *out_bytes);
+zipccl_status zipccl_moe_layer(const zipccl_moe_layer_args *args, const zipccl_route_options *options, void *d_ws,
+                               uint64_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -48,7 +48,7 @@ EXPORTED_SYMBOLS = [
     "zipccl_moe_route", "zipccl_moe_route_backward", "zipccl_moe_plan_workspace_bytes", "zipccl_moe_plan",
     "zipccl_moe_dispatch", "zipccl_moe_dispatch_backward", "zipccl_moe_combine", "zipccl_moe_combine_backward",
     "zipccl_adamw_step", "zipccl_moe_quantize", "zipccl_moe_quantize_columns", "zipccl_moe_quantize_weights",
-    "zipccl_moe_matmul", "zipccl_moe_status",
+    "zipccl_moe_matmul", "zipccl_moe_status", "zipccl_moe_layer_workspace_bytes", "zipccl_moe_layer",
 ]
 
 _lock = threading.Lock()
@@ -412,7 +412,7 @@ from .operators_abi import __all__ as _abi_names  # noqa: E402
 _tensor_names = ["MoePlan", "moe_route", "moe_route_backward", "moe_plan", "moe_dispatch", "moe_dispatch_backward",
                  "moe_combine", "moe_combine_backward", "adamw_step", "adamw_state", "ADAMW_BLOCK",
                  "Fp8Blocks", "FP8_BLOCK", "moe_quantize", "moe_quantize_columns", "moe_quantize_weights",
-                 "moe_matmul", "moe_matmul_backward", "moe_matmul_backward_weights", "moe_status"]
+                 "moe_matmul", "moe_matmul_backward", "moe_matmul_backward_weights", "moe_status", "moe_layer"]
 __all__ += [*_abi_names, *_tensor_names]
 
 

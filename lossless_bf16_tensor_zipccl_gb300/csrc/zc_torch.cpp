@@ -633,11 +633,105 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A matrix of weights for each expert: plain, or 8-bit blocks.
+struct Matrices {
+  const void* at;
+  const uint8_t* scales = nullptr;
+  uint64_t stride;
+  IntArrayRef shape;
+  bool small;
+  Tensor held, held_scales;
+  Matrices(PyObject* o, ScalarType type, c10::Device device, const char* what) {
+    small = PyTuple_Check(o);
+    if (small) {
+      const Blocks b = blocks(o, what);
+      if (b.codes.dim() != 3) refuse(PyExc_ValueError, "%s: expected three dimensions", what);
+      if (!b.codes.is_cuda() || b.codes.device() != device) refuse(PyExc_ValueError, "%s: expected a tensor on the device of the call's others", what);
+      plain(b.scales, ScalarType::Float8_e8m0fnu, {b.codes.size(0), block_count(b.codes.size(1)), block_count(b.codes.size(2))}, device, what);
+      held = b.codes;
+      held_scales = b.scales;
+      stride = code_stride(held, what);
+      scales = bytes(held_scales);
+    } else {
+      held = tensor(o, what);
+      plain(held, type, held.sizes(), device, what);
+      if (held.dim() != 3) refuse(PyExc_ValueError, "%s: expected three dimensions", what);
+      stride = (uint64_t)held.size(2);
+    }
+    at = held.const_data_ptr();
+    shape = held.sizes();
+  }
+};
+
+// x, router, up, down, <route options>, bias, mask, activation, residual, out, weights, ids, ws, stream
+PyObject* layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 20);
+  no_autograd("moe_layer", {a[0], a[1], a[2], a[3], a[14]});
+  const zipccl_route_options o = route_options(a + 4);
+  const Tensor &x = tensor(a[0], "x"), &router = tensor(a[1], "router");
+  zipccl_moe_layer_args l{};
+  l.type = value_type(x, "x");
+  l.router_type = value_type(router, "router");
+  l.x_stride = row_stride(x, "x");
+  const int64_t tokens = x.size(0), hidden = x.size(1), k = o.top_k;
+  if (bad_top_k(k)) return refused();
+  const c10::Device device = x.device();
+  two_dims(router, "router");
+  const int64_t experts = router.size(0);
+  plain(router, router.scalar_type(), {experts, hidden}, device, "router");
+  if (router.scalar_type() != x.scalar_type() && router.scalar_type() != ScalarType::Float)
+    refuse(PyExc_TypeError, "router: expected the type of x or float32");
+  const Matrices up(a[2], x.scalar_type(), device, "up"), down(a[3], x.scalar_type(), device, "down");
+  if (up.small != down.small) refuse(PyExc_TypeError, "up and down: expected both in 8-bit blocks or neither");
+  const int64_t inner = down.shape[2], rows = up.shape[1];
+  if (up.shape[0] != experts || down.shape[0] != experts || up.shape[2] != hidden || down.shape[1] != hidden ||
+      (rows != inner && rows != 2 * inner))
+    refuse(PyExc_ValueError, "up and down: expected [experts, inner or 2 inner, hidden] and [experts, hidden, inner]");
+  l.gated = rows != inner;
+  l.weight_bits = up.small ? 8 : 8 * (int)x.element_size();
+  l.d_bias = static_cast<const float*>(optional(a[11], ScalarType::Float, {experts}, device, "bias"));
+  if (a[12] != Py_None) {
+    const Tensor& m = tensor(a[12], "mask");
+    l.d_mask = static_cast<const uint8_t*>(plain(m, m.scalar_type() == ScalarType::Byte ? ScalarType::Byte : ScalarType::Bool, {tokens}, device, "mask").const_data_ptr());
+  }
+  l.activation = (int32_t)integer(a[13]);
+  l.d_residual = optional(a[14], x.scalar_type(), {tokens, hidden}, device, "residual");
+  uint64_t need = 0;
+  const zipccl_status sized = zipccl_moe_layer_workspace_bytes((uint64_t)tokens, (uint32_t)k, (uint64_t)inner, &need);
+  if (sized != ZIPCCL_OK) return PyLong_FromLong(sized);
+  const Call call(device, a[19]);
+  const Tensor y = call.result(a[15], {tokens, hidden}, x.scalar_type(), "out");
+  const Tensor weights = call.result(a[16], {tokens, k}, ScalarType::Float, "weights");
+  const Tensor ids = call.result(a[17], {tokens, k}, ScalarType::Int, "ids");
+  Tensor ws;
+  if (a[18] != Py_None) ws = tensor(a[18], "ws");
+  if (!ws.defined() || ws.nbytes() < need) ws = call.scratch({(int64_t)need}, ScalarType::Byte);
+  plain(ws, ws.scalar_type(), ws.sizes(), device, "ws");
+  l.d_x = x.const_data_ptr();
+  l.d_router = router.const_data_ptr();
+  l.d_up = up.at;
+  l.d_down = down.at;
+  l.d_up_scales = up.scales;
+  l.d_down_scales = down.scales;
+  l.d_y = y.data_ptr();
+  l.d_weights = static_cast<float*>(weights.data_ptr());
+  l.d_ids = static_cast<int32_t*>(ids.data_ptr());
+  l.tokens = (uint64_t)tokens;
+  l.hidden = (uint64_t)hidden;
+  l.inner = (uint64_t)inner;
+  l.up_stride = up.stride;
+  l.down_stride = down.stride;
+  l.experts = (uint32_t)std::min<int64_t>(experts, UINT32_MAX);
+  return answer(zipccl_moe_layer(&l, &o, ws.data_ptr(), ws.nbytes(), call.stream), {y, weights, ids});
+  END_HANDLE_TH_ERRORS
+}
+
 #define ZC_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ZC_METHOD(route),             ZC_METHOD(route_backward), ZC_METHOD(plan),
                          ZC_METHOD(dispatch),          ZC_METHOD(dispatch_backward), ZC_METHOD(combine),
                          ZC_METHOD(combine_backward),  ZC_METHOD(adamw),          ZC_METHOD(quantize),
-                         ZC_METHOD(quantize_columns),  ZC_METHOD(quantize_weights), ZC_METHOD(matmul),
+                         ZC_METHOD(quantize_columns),  ZC_METHOD(quantize_weights), ZC_METHOD(matmul),            ZC_METHOD(layer),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_zipccl_torch", "Operator calls of libzipccl on torch tensors.", -1, methods};
 

@@ -30,13 +30,14 @@ from . import _build, _check, load
 __all__ = ["ADAMW_BLOCK", "MoePlan", "moe_route", "moe_route_backward", "moe_plan", "moe_dispatch",
            "moe_dispatch_backward", "moe_combine", "moe_combine_backward", "adamw_step", "adamw_state", "FP8_BLOCK",
            "Fp8Blocks", "moe_quantize", "moe_quantize_columns", "moe_quantize_weights", "moe_matmul",
-           "moe_matmul_backward", "moe_matmul_backward_weights", "moe_status"]
+           "moe_matmul_backward", "moe_matmul_backward_weights", "moe_status", "moe_layer"]
 
 ADAMW_BLOCK = 256  # values that share one scale of an 8-bit state
 FP8_BLOCK = 128    # values, rows or both that share one scale of 8-bit operands
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _GROUP_SCORES = {"max": 0, "top2": 1}
+_ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _FORWARD, _BACKWARD, _WEIGHTS = range(3)
 
@@ -205,6 +206,23 @@ def moe_status(stream=None) -> None:
     current device has run out since the last such call (synchronizes)."""
     handle = torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
     _check(load().zipccl_moe_status(handle), "zipccl_moe_status")
+
+
+def moe_layer(x, router, up, down, top_k: int, *, score: str = "softmax", bias=None, groups: int = 1,
+              groups_kept: int = 1, group_score: str = "max", renormalize: bool = True, scale: float = 1.0, mask=None,
+              activation: str = "silu", residual=None, out=None, weights=None, ids=None, ws=None, stream=None):
+    """A whole layer for up to 32 tokens, in two kernels: (y [tokens, hidden],
+    weights and ids [tokens, top_k] as ``moe_route`` gives them for the logits
+    x @ router.T; see zipccl_moe_layer).  ``router`` is [experts, hidden], of x's
+    type or float32; ``up`` [experts, inner or 2 * inner, hidden] (twice as many
+    rows: the first half is the gate's) and ``down`` [experts, hidden, inner], both
+    of x's type or both ``Fp8Blocks`` from ``moe_quantize_weights``;
+    ``activation`` "silu", "gelu" or "relu".  x may have any row stride.  For more
+    tokens: route, plan, dispatch, ``moe_matmul``, combine."""
+    return _done(_native.layer(x, router, up, down, top_k, _choice(_SCORES, "score", score), renormalize, scale, groups,
+                               groups_kept, _choice(_GROUP_SCORES, "group_score", group_score), bias, mask,
+                               _choice(_ACTIVATIONS, "activation", activation), residual, out, weights, ids, ws,
+                               _handle(stream)), "zipccl_moe_layer")
 
 
 def adamw_state(param, bits: int = 32):

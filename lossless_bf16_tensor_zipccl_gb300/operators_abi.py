@@ -13,10 +13,11 @@ __all__ = [
     "zipccl_moe_dispatch", "zipccl_moe_dispatch_backward", "zipccl_moe_combine", "zipccl_moe_combine_backward",
     "zipccl_adamw_step", "MATMUL_FORWARD", "MATMUL_BACKWARD", "MATMUL_WEIGHTS", "Fp8BlocksArg",
     "zipccl_moe_quantize", "zipccl_moe_quantize_columns", "zipccl_moe_quantize_weights", "zipccl_moe_matmul",
-    "zipccl_moe_status",
+    "zipccl_moe_status", "LAYER_MAX_TOKENS", "MoeLayerArgs", "zipccl_moe_layer_workspace_bytes", "zipccl_moe_layer",
 ]
 
 TYPE_F32, TYPE_BF16, TYPE_F16 = range(3)
+LAYER_MAX_TOKENS = 32
 MATMUL_FORWARD, MATMUL_BACKWARD, MATMUL_WEIGHTS = range(3)
 
 
@@ -41,6 +42,15 @@ class Fp8BlocksArg(ctypes.Structure):
     _fields_ = [("d_codes", ctypes.c_void_p), ("d_scales", ctypes.c_void_p), ("stride", ctypes.c_uint64)]
 
 
+class MoeLayerArgs(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("d_x", "d_router", "d_up", "d_down", "d_residual", "d_up_scales", "d_down_scales", "d_bias", "d_mask",
+                 "d_y", "d_weights", "d_ids")] + [
+                (name, ctypes.c_uint64) for name in ("tokens", "hidden", "inner", "x_stride", "up_stride", "down_stride")] + [
+                ("experts", ctypes.c_uint32)] + [
+                (name, ctypes.c_int32) for name in ("type", "router_type", "weight_bits", "gated", "activation")]
+
+
 def declare(L) -> None:
     """Argument types of the library's operator calls (used by ``load``)."""
     u64, u32, i32, vp = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int, ctypes.c_void_p
@@ -61,11 +71,13 @@ def declare(L) -> None:
     blocks = ctypes.POINTER(Fp8BlocksArg)
     L.zipccl_moe_matmul.argtypes = [i32, blocks, blocks, u64, u64, u64, vp, u32, vp, i32, u64, vp]
     L.zipccl_moe_status.argtypes = [vp]
+    L.zipccl_moe_layer_workspace_bytes.argtypes = [u64, u32, u64, ctypes.POINTER(u64)]
+    L.zipccl_moe_layer.argtypes = [ctypes.POINTER(MoeLayerArgs), ro, vp, u64, vp]
     for name in ("zipccl_moe_route", "zipccl_moe_route_backward", "zipccl_moe_plan_workspace_bytes",
                  "zipccl_moe_plan", "zipccl_moe_dispatch", "zipccl_moe_dispatch_backward", "zipccl_moe_combine",
                  "zipccl_moe_combine_backward", "zipccl_adamw_step",
                  "zipccl_moe_quantize", "zipccl_moe_quantize_columns", "zipccl_moe_quantize_weights",
-                 "zipccl_moe_matmul", "zipccl_moe_status"):
+                 "zipccl_moe_matmul", "zipccl_moe_status", "zipccl_moe_layer_workspace_bytes", "zipccl_moe_layer"):
         getattr(L, name).restype = ctypes.c_int
 
 
@@ -150,3 +162,14 @@ def zipccl_moe_matmul(form: int, a: Fp8BlocksArg, b: Fp8BlocksArg, rows: int, in
 
 def zipccl_moe_status(stream: int) -> int:
     return load().zipccl_moe_status(stream)
+
+
+def zipccl_moe_layer_workspace_bytes(tokens: int, top_k: int, inner: int) -> int:
+    out = ctypes.c_uint64()
+    _check(load().zipccl_moe_layer_workspace_bytes(int(tokens), int(top_k), int(inner), ctypes.byref(out)),
+           "zipccl_moe_layer_workspace_bytes")
+    return int(out.value)
+
+
+def zipccl_moe_layer(args: MoeLayerArgs, options: RouteOptions, d_ws: int, ws_bytes: int, stream: int) -> int:
+    return load().zipccl_moe_layer(args, options, d_ws, ws_bytes, stream)
