@@ -21,7 +21,6 @@
 // issues the products; 2 lays the scales out (128 rows x 4 bytes, four blocks of
 // the sum a time); 3 clears what a chunk's last block of rows reads of the next
 // chunk (gradient of the weights); 4 to 7 write results.
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -345,23 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
 }
 
 // ---------------------------------------------------------------- host
-using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-Encode encoder() {
-  static std::atomic<void*> found{nullptr};
-  void* f = found.load(std::memory_order_acquire);
-  if (!f) {
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      return nullptr;
-    found.store(f, std::memory_order_release);
-  }
-  return reinterpret_cast<Encode>(f);
-}
-
 // Map of codes [matrices][rows][cols]; a copy takes 128 bytes of `box` rows.  Rows
 // and columns beyond the matrix read as zeros.
 bool code_map(CUtensorMap* m, const zipccl_fp8_blocks* x, uint64_t cols, uint64_t rows, uint64_t matrices, uint32_t dims,
@@ -467,16 +449,10 @@ zipccl_status zipccl_moe_matmul(int form, const zipccl_fp8_blocks* a, const zipc
 }
 
 zipccl_status zipccl_moe_status(void* stream) {
-  unsigned int v = 0, zero = 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemcpyFromSymbolAsync(&v, g_wait_ran_out, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return ZIPCCL_ERR_CUDA;
-  if (!v) return ZIPCCL_OK;
-  if (cudaMemcpyToSymbolAsync(g_wait_ran_out, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return ZIPCCL_ERR_CUDA;
-  return ZIPCCL_ERR_TIMEOUT;
+  bool ran_out = false;
+  if (take_flag(g_wait_ran_out, s, &ran_out) != cudaSuccess || layer_waits(s, &ran_out) != cudaSuccess) return ZIPCCL_ERR_CUDA;
+  return ran_out ? ZIPCCL_ERR_TIMEOUT : ZIPCCL_OK;
 }
 
 }  // extern "C"

@@ -2,8 +2,11 @@
 // tensor maps, block-scaled 8-bit products with sums in tensor memory, waits
 // with an end.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "zc_device.cuh"
 
@@ -20,6 +23,22 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
       : "memory");
   return done ? true : mbar_wait(bar, parity);
 }
+
+// Whether a wait has run out, from a kernel's word of it, which is cleared.
+template <class Word>
+cudaError_t take_flag(const Word& word, cudaStream_t s, bool* ran_out) {
+  const Word zero = 0;
+  Word v = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, word, sizeof(v), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && v) {
+    *ran_out = true;
+    e = cudaMemcpyToSymbolAsync(word, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
+  return e;
+}
+cudaError_t layer_waits(cudaStream_t s, bool* ran_out);  // zc_layer.cu
 
 // ---- tensor maps
 __device__ __forceinline__ void tma_prefetch(const void* map) {
@@ -106,6 +125,34 @@ __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint
       " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
       "l"(a), "l"(b), "r"(word), "r"(scale_a), "r"(scale_b), "r"((uint32_t)add)
       : "memory");
+}
+
+// ---------------------------------------------------------------- host
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline Encode encoder() {
+  static std::atomic<void*> found{nullptr};
+  void* f = found.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      return nullptr;
+    found.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<Encode>(f);
+}
+
+// Map of rows of `bytes` bytes, `stride` bytes apart (multiples of 16, as the start
+// is), as 64-bit words; a copy takes `words` of `box` rows.
+inline bool word_map(CUtensorMap* m, const void* at, uint64_t bytes, uint64_t rows, uint64_t stride, uint32_t words, uint32_t box) {
+  const Encode f = encoder();
+  const cuuint64_t size[2] = {(bytes + 15) / 16 * 2, rows}, strides[1] = {stride};
+  const cuuint32_t boxes[2] = {words, box}, steps[2] = {1, 1};
+  return f && f(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void*>(at), size, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace zc
