@@ -6,7 +6,10 @@
 // as they are (one for 32 places of the sum: the same for four instructions), so
 // nothing is done between the operands' arrival and the result.
 //
-// A tile of the result is 128 lanes x up to 256 columns of tensor memory.  The
+// A tile of the result is 256 lanes x up to 256 columns, made by the tensor cores of
+// a pair of multiprocessors together: each has 128 of the lanes and loads half of
+// the columns' operand, so that a multiprocessor takes 64 bytes from the L2 cache
+// for the work of a cycle (alone it would take 96).  The
 // lanes are the matrices' rows (outer or inner places), the columns the chunk's
 // rows: a chunk may have any number of rows, and the columns of an instruction may
 // be any multiple of 32, so that a chunk's end costs at most 31 columns, where the
@@ -14,13 +17,17 @@
 // places, columns the outer ones, and the chunk's rows are summed over.
 // The result thus lies with its contiguous index along the lanes.
 //
+// Two tiles have room in tensor memory beside the scales but for 32 columns: the
+// next tile's first 32 columns are the last 32 of a full one, which are read
+// first.
+//
 // The weights are read along the sum forward and across it backward, from the
 // same codes: blocks of 128 x 128 serve both.
 //
-// Warps: 0 loads tiles through tensor maps, four stages of 128 places ahead; 1
-// issues the products; 2 lays the scales out (128 rows x 4 bytes, four blocks of
-// the sum a time); 3 clears what a chunk's last block of rows reads of the next
-// chunk (gradient of the weights); 4 to 7 write results.
+// Warps: 0 loads tiles through tensor maps, five stages of 128 places ahead; 1 (of
+// the leading block) issues the products; 2 lays the scales out (128 rows x 4
+// bytes, four blocks of the sum a time); 3 clears what a chunk's last block of rows
+// reads of the next chunk (gradient of the weights); 4 to 11 write results.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -34,13 +41,15 @@
 namespace zc {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr uint32_t kLanes = 128, kColumns = 256, kPlaces = 128;  // of a tile; places of the sum in a stage
-constexpr uint32_t kStages = 4;
-constexpr uint32_t kBytesA = kLanes * kPlaces, kBytesB = kColumns * kPlaces, kStageBytes = kBytesA + kBytesB;
+constexpr int kWriters = 8, kThreads = (4 + kWriters) * 32;
+constexpr uint32_t kLanes = 256, kOwnLanes = 128;                   // of a tile, and those of a block
+constexpr uint32_t kColumns = 256, kOwnColumns = 128, kPlaces = 128;  // columns; places of the sum in a stage
+constexpr uint32_t kStages = 5;
+constexpr uint32_t kBytesA = kOwnLanes * kPlaces, kBytesB = kOwnColumns * kPlaces, kStageBytes = kBytesA + kBytesB;
 constexpr uint32_t kScaleSets = 4, kScaleBytes = 512 * 3;  // four blocks' scales: 128 lanes, 256 columns
-constexpr uint32_t kBoxRows = 32;
-constexpr uint32_t kScaleColumns = 256;  // tensor memory: where scales begin, 16 columns for each of two sets
+constexpr uint32_t kBoxRows = 16;
+// Tensor memory: sums from columns 0 and 224 on, scales behind them, 16 columns for each of two sets.
+constexpr uint32_t kSecond = 224, kScaleColumns = kSecond + kColumns;
 
 __device__ unsigned int g_wait_ran_out;
 
@@ -55,12 +64,15 @@ struct MatmulArgs {
   uint32_t lanes, columns, sum;          // of the result and the sum (WEIGHTS: columns; sum unused; else columns unused)
   uint32_t rows, chunks, lane_tiles, column_tiles;
   uint32_t b_blocks;                     // scales of a row
+  bool wide;                             // rows of the result start at multiples of 16 bytes
 };
 
 struct Shared {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
   alignas(128) uint8_t scales[kScaleSets][kScaleBytes];
-  uint64_t full[kStages], empty[kStages], scales_full[kScaleSets], scales_empty[kScaleSets], clear, cleared, done, taken;
+  alignas(16) uint8_t turned[kWriters][32 * 32 * 4];  // results of a writing warp, the other way round
+  uint64_t full[kStages], empty[kStages], scales_full[kScaleSets], scales_empty[kScaleSets], clear, cleared;
+  uint64_t done[2], shared_taken[2], taken[2];
   uint32_t tmem;
   uint32_t first[kMaxChunks + 2];  // first row of each chunk; the rows behind the last are one more
   uint32_t tiles[kMaxChunks + 2];  // tiles of rows before each (WEIGHTS: blocks of the scales)
@@ -68,11 +80,11 @@ struct Shared {
 
 struct Tile {
   uint32_t chunk, row, count;   // rows of the tile (WEIGHTS: of the chunk)
-  uint32_t lane0, column0, columns, blocks;
+  uint32_t lane0, column0, columns, width, blocks;  // lane0: of this block; width: columns of the instructions
 };
 
 template <bool kWeights>
-__device__ __forceinline__ Tile tile_of(const MatmulArgs& a, const Shared& s, uint32_t t) {
+__device__ __forceinline__ Tile tile_of(const MatmulArgs& a, const Shared& s, uint32_t t, uint32_t rank) {
   Tile x;
   if constexpr (kWeights) {
     const uint32_t per = a.lane_tiles * a.column_tiles;
@@ -102,7 +114,36 @@ __device__ __forceinline__ Tile tile_of(const MatmulArgs& a, const Shared& s, ui
     x.columns = x.count;
     x.blocks = lo < a.chunks && x.count ? (a.sum + kPlaces - 1) / kPlaces : 0;
   }
+  x.lane0 += rank * kOwnLanes;
+  x.width = (x.columns + 31) / 32 * 32;
   return x;
+}
+
+// 32 columns of a warp's 32 lanes, from column c of `count`: out + column * stride
+// + lane.  Where rows are wide they are turned in shared memory first, so that a
+// warp writes 16 bytes a lane, 64 or 128 consecutive ones; `lanes`: those in range.
+template <class T>
+__device__ __forceinline__ void write_columns(const uint32_t (&v)[32], T* out, uint64_t stride, uint32_t c, uint32_t count, uint32_t lanes,
+                                              bool wide, uint8_t* turned) {
+  const uint32_t lane = threadIdx.x % 32;
+  if (wide && lanes >= 32) {
+    T* s = reinterpret_cast<T*>(turned);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i * 32 + lane] = from_float<T>(__uint_as_float(v[i]));
+    __syncwarp();
+    constexpr uint32_t kPer = 16 / sizeof(T), kAcross = 32 / kPer;  // values of a lane, lanes of a row
+#pragma unroll
+    for (uint32_t i = 0; i < 32; i += 32 / kAcross) {
+      const uint32_t row = i + lane / kAcross, at = lane % kAcross * kPer;
+      const uint4 q = *reinterpret_cast<const uint4*>(s + row * 32 + at);
+      if (c + row < count) *reinterpret_cast<uint4*>(out + (c + row) * stride + at) = q;
+    }
+    __syncwarp();
+  } else if (lane < lanes) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c + i < count) out[(c + i) * stride + lane] = from_float<T>(__uint_as_float(v[i]));
+  }
 }
 
 template <class T, int kForm>
@@ -110,17 +151,17 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
   constexpr bool kWeights = kForm == ZIPCCL_MATMUL_WEIGHTS;
   constexpr bool kAcrossA = kForm != ZIPCCL_MATMUL_FORWARD, kAcrossB = kWeights;
   extern __shared__ uint8_t s_raw[];
-  Shared& s = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  Shared& s = *reinterpret_cast<Shared*>(s_raw + ((1024 - (smem_addr(s_raw) & 1023)) & 1023));
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, rank = cluster_rank();
+  const uint32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   if (threadIdx.x == 0) {
     tma_prefetch(&a.a);
     tma_prefetch(&a.b);
     for (uint32_t i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
-    for (uint32_t i = 0; i < kScaleSets; ++i) mbar_init(&s.scales_full[i], 1), mbar_init(&s.scales_empty[i], 1);
+    for (uint32_t i = 0; i < kScaleSets; ++i) mbar_init(&s.scales_full[i], 2), mbar_init(&s.scales_empty[i], 1);
     mbar_init(&s.clear, 1);
-    mbar_init(&s.cleared, 1);
-    mbar_init(&s.done, 1);
-    mbar_init(&s.taken, 128);
+    mbar_init(&s.cleared, 2);
+    for (uint32_t i = 0; i < 2; ++i) mbar_init(&s.done[i], 1), mbar_init(&s.shared_taken[i], 2 * kWriters), mbar_init(&s.taken[i], 2 * kWriters);
   }
   if (warp == 1) tmem_alloc(&s.tmem, 512);
   after_previous();
@@ -155,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
   }
   tmem_fence_before();
   __syncthreads();
+  cluster_sync();  // both blocks' barriers and tensor memory are there
   tmem_fence_after();
   const uint32_t tmem = s.tmem;
   const uint32_t total = kWeights ? a.chunks * a.lane_tiles * a.column_tiles : s.tiles[a.chunks + 1] * a.lane_tiles;
@@ -163,44 +205,53 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
   if (warp == 0) {
     if (lane == 0) {
       uint32_t n = 0;  // stages filled
-      for (uint32_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        const Tile x = tile_of<kWeights>(a, s, t);
-        const uint32_t pieces = kWeights ? (x.columns + kPlaces - 1) / kPlaces : (x.columns + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = kBytesA + pieces * (kWeights ? kPlaces * kPlaces : kBoxRows * kPlaces);
+      for (uint32_t t = pair; t < total && ok; t += pairs) {
+        const Tile x = tile_of<kWeights>(a, s, t, rank);
+        const uint32_t half = x.width / 2, column0 = x.column0 + rank * half;
+        const uint32_t pieces = kWeights ? 1 : half / kBoxRows;
+        const uint32_t bytes = kBytesA + (kWeights ? kBytesB : half * kPlaces);
         for (uint32_t k = 0; k < x.blocks; ++k, ++n) {
           const uint32_t st = n % kStages;
-          if (!(ok = wait_phase(&s.empty[st], (n / kStages & 1) ^ 1))) break;
+          if (!(ok = wait_cluster(&s.empty[st], (n / kStages & 1) ^ 1))) break;
           uint8_t* to = s.stage[st];
-          mbar_arrive_expect_tx(&s.full[st], bytes);
+          if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * bytes);
+          const uint32_t full = at_rank(&s.full[st], 0);
           const int32_t at = (int32_t)(k * kPlaces);
-          if constexpr (kForm == ZIPCCL_MATMUL_FORWARD) tma_load_3d(to, &a.a, at, x.lane0, x.chunk, &s.full[st]);
-          else if constexpr (kForm == ZIPCCL_MATMUL_BACKWARD) tma_load_3d(to, &a.a, x.lane0, at, x.chunk, &s.full[st]);
-          else tma_load_3d(to, &a.a, x.lane0, x.row + at, 0, &s.full[st]);
+          if constexpr (kForm == ZIPCCL_MATMUL_FORWARD) pair_load_3d(to, &a.a, at, x.lane0, x.chunk, full);
+          else if constexpr (kForm == ZIPCCL_MATMUL_BACKWARD) pair_load_3d(to, &a.a, x.lane0, at, x.chunk, full);
+          else pair_load_3d(to, &a.a, x.lane0, x.row + at, 0, full);
           to += kBytesA;
-          for (uint32_t i = 0; i < pieces; ++i) {
-            if constexpr (kWeights) tma_load_2d(to + i * kPlaces * kPlaces, &a.b, x.column0 + i * kPlaces, x.row + at, &s.full[st]);
-            else tma_load_2d(to + i * kBoxRows * kPlaces, &a.b, at, x.row + i * kBoxRows, &s.full[st]);
+          if constexpr (kWeights) {
+            pair_load_2d(to, &a.b, column0, x.row + at, full);
+          } else {
+            for (uint32_t i = 0; i < pieces; ++i) pair_load_2d(to + i * kBoxRows * kPlaces, &a.b, at, x.row + rank * half + i * kBoxRows, full);
           }
         }
       }
-      // a block that gives up does not end under its own copies
-      for (uint32_t i = n > kStages ? n - kStages : 0; !ok && i < n; ++i) wait_phase(&s.full[i % kStages], i / kStages & 1);
+      // a block that gives up does not end under copies: the leading one waits for both
+      for (uint32_t i = n > kStages ? n - kStages : 0; rank == 0 && !ok && i < n; ++i) wait_cluster(&s.full[i % kStages], i / kStages & 1);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t n = 0, sets = 0, tiles = 0, clears = 0;
-      for (uint32_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        const Tile x = tile_of<kWeights>(a, s, t);
+    if (lane == 0 && rank == 0) {
+      uint32_t n = 0, sets = 0, tiles = 0, clears = 0, columns = 0;
+      for (uint32_t t = pair; t < total && ok; t += pairs) {
+        const Tile x = tile_of<kWeights>(a, s, t, rank);
         if (x.blocks == 0) continue;
-        if (!(ok = wait_phase(&s.taken, (tiles & 1) ^ 1))) break;
+        const uint32_t buffer = tiles & 1, turn = tiles >> 1;
+        if (!(ok = wait_cluster(&s.taken[buffer], (turn & 1) ^ 1))) break;
+        // columns that the tile before has in the way
+        if (tiles && (buffer ? columns : x.columns) > kSecond &&
+            !(ok = wait_cluster(&s.shared_taken[buffer ^ 1], ((tiles - 1) >> 1) & 1)))
+          break;
+        columns = x.columns;
         tmem_fence_after();
-        const uint32_t word = product_word((x.columns + 31) / 32 * 32, kAcrossA, kAcrossB);
+        const uint32_t sums = tmem + buffer * kSecond, word = product_word(x.width, kAcrossA, kAcrossB);
         uint32_t scales = 0;
         for (uint32_t k = 0; k < x.blocks; ++k, ++n) {
           const uint32_t st = n % kStages;
           if (k % 4 == 0) {
             const uint32_t set = sets % kScaleSets;
-            if (!(ok = wait_phase(&s.scales_full[set], sets / kScaleSets & 1))) break;
+            if (!(ok = wait_cluster(&s.scales_full[set], sets / kScaleSets & 1))) break;
             tmem_fence_after();
             scales = tmem + kScaleColumns + sets % 2 * 16;
             const uint32_t from = smem_addr(s.scales[set]);
@@ -210,32 +261,33 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
             tensor_commit(&s.scales_empty[set]);
             ++sets;
           }
-          if (!(ok = wait_phase(&s.full[st], n / kStages & 1))) break;
+          if (!(ok = wait_cluster(&s.full[st], n / kStages & 1))) break;
           uint32_t steps = 4;
           if (kWeights && k + 1 == x.blocks && x.count % kPlaces) {
             steps = (x.count % kPlaces + 31) / 32;
             if (x.count % 32) {
-              mbar_arrive(&s.clear);
-              if (!(ok = wait_phase(&s.cleared, clears & 1))) break;
+              arrive_at(at_rank(&s.clear, 0));
+              arrive_at(at_rank(&s.clear, 1));
+              if (!(ok = wait_cluster(&s.cleared, clears & 1))) break;
               ++clears;
             }
           }
           tmem_fence_after();
           const uint32_t at = smem_addr(s.stage[st]);
           for (uint32_t i = 0; i < steps; ++i)
-            product(tmem, operand(at + i * (kAcrossA ? 4096 : 32), 0), operand(at + kBytesA + i * (kAcrossB ? 4096 : 32), kPlaces * kPlaces),
+            product(sums, operand(at + i * (kAcrossA ? 4096 : 32), 0), operand(at + kBytesA + i * (kAcrossB ? 4096 : 32), 0),
                     with_scale(word, k % 4), scales, scales + 4, k + i > 0);
           tensor_commit(&s.empty[st]);
         }
         if (!ok) break;
-        tensor_commit(&s.done);
+        tensor_commit(&s.done[buffer]);
         ++tiles;
       }
     }
   } else if (warp == 2) {
     uint32_t sets = 0;
-    for (uint32_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const Tile x = tile_of<kWeights>(a, s, t);
+    for (uint32_t t = pair; t < total && ok; t += pairs) {
+      const Tile x = tile_of<kWeights>(a, s, t, rank);
       for (uint32_t k0 = 0; k0 < x.blocks; k0 += 4, ++sets) {
         const uint32_t set = sets % kScaleSets, left = min(4u, x.blocks - k0);
         // word j of a lane: row 32 j + lane, a byte for each of the four blocks
@@ -254,10 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
               if (i < left && at < wide) w[j] |= (uint32_t)p[(uint64_t)i * wide] << (8 * i);
           }
         } else {
-          const uint8_t* p = a.scales_a + x.chunk * a.a_matrix + (uint64_t)(x.lane0 / kLanes) * a.a_lane + (uint64_t)k0 * a.a_block;
+          const uint8_t* p = a.scales_a + x.chunk * a.a_matrix + (uint64_t)(x.lane0 / kOwnLanes) * a.a_lane + (uint64_t)k0 * a.a_block;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (i < left) w[0] |= (uint32_t)p[(uint64_t)i * a.a_block] << (8 * i);
+            if (i < left && x.lane0 < a.lanes) w[0] |= (uint32_t)p[(uint64_t)i * a.a_block] << (8 * i);
           w[1] = w[2] = w[3] = w[0];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -268,67 +320,78 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
               if (i < left && r < x.count) w[4 + j] |= (uint32_t)q[i] << (8 * i);
           }
         }
-        if (!(ok = wait_phase(&s.scales_empty[set], (sets / kScaleSets & 1) ^ 1))) break;
+        if (!(ok = wait_cluster(&s.scales_empty[set], (sets / kScaleSets & 1) ^ 1))) break;
         uint4* to = reinterpret_cast<uint4*>(s.scales[set]) + lane;
 #pragma unroll
         for (int j = 0; j < 3; ++j) to[32 * j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.scales_full[set]);
+        if (lane == 0) arrive_at(at_rank(&s.scales_full[set], 0));
       }
     }
   } else if (warp == 3) {
     if constexpr (kWeights) {
       uint32_t n = 0, clears = 0;
-      for (uint32_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        const Tile x = tile_of<kWeights>(a, s, t);
+      for (uint32_t t = pair; t < total && ok; t += pairs) {
+        const Tile x = tile_of<kWeights>(a, s, t, rank);
         n += x.blocks;
         if (x.count % 32 == 0) continue;
-        // warp 1 asks for it when the stage has arrived, and goes on when it is done
-        const uint32_t st = (n - 1) % kStages;
-        if (!(ok = wait_phase(&s.clear, clears & 1)) || !(ok = wait_phase(&s.full[st], (n - 1) / kStages & 1))) break;
+        // the leading block's warp 1 asks for it when the stage has arrived in both, and goes on when it is done
+        if (!(ok = wait_cluster(&s.clear, clears & 1))) break;
         ++clears;
-        const uint32_t from = x.count % kPlaces, upto = (from + 31) / 32 * 32;
+        const uint32_t st = (n - 1) % kStages, from = x.count % kPlaces, upto = (from + 31) / 32 * 32;
         for (uint32_t i = from * 8 + lane; i < upto * 8; i += 32)
 #pragma unroll
-          for (int piece = 0; piece < 3; ++piece)
-            reinterpret_cast<uint4*>(s.stage[st] + piece * kPlaces * kPlaces)[i] = make_uint4(0, 0, 0, 0);
+          for (int piece = 0; piece < 2; ++piece)
+            reinterpret_cast<uint4*>(s.stage[st] + piece * kBytesA)[i] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.cleared);
+        if (lane == 0) arrive_at(at_rank(&s.cleared, 0));
       }
     }
   } else {
-    const uint32_t quarter = warp % 4;
+    // two warps for each quarter of the lanes, every other 32 columns each.  Columns
+    // that the next tile's sums will lie in come first: in the first buffer the last
+    // 32 of a full tile, in the second the first 32.
+    const uint32_t quarter = warp % 4, other = (warp - 4) / 4;
     uint32_t tiles = 0;
-    for (uint32_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const Tile x = tile_of<kWeights>(a, s, t);
-      const uint32_t place = x.lane0 + quarter * 32 + lane;
+    for (uint32_t t = pair; t < total && ok; t += pairs) {
+      const Tile x = tile_of<kWeights>(a, s, t, rank);
+      const uint32_t place = x.lane0 + quarter * 32, lanes = place < a.lanes ? a.lanes - place : 0;
+      const uint32_t buffer = tiles & 1, sums = tmem + buffer * kSecond + (quarter << 21);
       T* out = static_cast<T*>(a.out) + place;
       if constexpr (kWeights) out += x.chunk * a.out_matrix + x.column0 * a.out_stride;
       else out += x.row * a.out_stride;
       if (x.blocks) {
-        if (!(ok = wait_phase(&s.done, tiles & 1))) break;
+        if (!(ok = wait_cluster(&s.done[buffer], (tiles >> 1) & 1))) break;
         tmem_fence_after();
       }
-      for (uint32_t c = 0; c < x.columns; c += 32) {
+      bool told = false;
+      const uint32_t parts = x.width / 32;
+      // (backwards in the first buffer)
+      for (uint32_t i = other; i < parts + other; i += 2) {
+        const bool mine = i < parts;
+        const uint32_t c = (buffer ? i : parts - 1 - i) * 32;
         uint32_t v[32];
-        if (x.blocks) {
-          tmem_load32(tmem + (quarter << 21) + c, v);
+        if (mine && x.blocks) {
+          tmem_load32(sums + c, v);
           tmem_wait_load();
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0;
+          for (int j = 0; j < 32; ++j) v[j] = 0;
         }
-        if (place < a.lanes) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < x.columns) out[(c + i) * a.out_stride] = from_float<T>(__uint_as_float(v[i]));
+        if (x.blocks && !told) {
+          told = true;
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_at(at_rank(&s.shared_taken[buffer], 0));
         }
+        if (mine) write_columns<T>(v, out, a.out_stride, c, x.columns, lanes, a.wide, s.turned[warp - 4]);
       }
       if (x.blocks) {
         tmem_fence_before();
-        mbar_arrive(&s.taken);
+        __syncwarp();
+        if (lane == 0) arrive_at(at_rank(&s.taken[buffer], 0));
         ++tiles;
       }
     }
@@ -337,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
+  cluster_sync();
   if (warp == 1) {
     tmem_fence_after();
     tmem_free(tmem, 512);
@@ -371,7 +435,15 @@ cudaError_t matmul_launch(const MatmulArgs& a, uint64_t tiles, cudaStream_t s) {
       return e;
     multiprocessors[dev].store(sms, std::memory_order_release);
   }
-  return launch(zc_matmul_kernel<T, kForm>, (uint32_t)std::min<uint64_t>(tiles, sms), kThreads, kSmem, s, a);
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 2, at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = 2 * (uint32_t)std::min<uint64_t>(tiles, sms / 2), cfg.blockDim = kThreads, cfg.dynamicSmemBytes = kSmem, cfg.stream = s;
+  cfg.attrs = at, cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, zc_matmul_kernel<T, kForm>, a);
 }
 
 template <class T>
@@ -418,6 +490,7 @@ zipccl_status zipccl_moe_matmul(int form, const zipccl_fp8_blocks* a, const zipc
   m.chunks = experts;
   m.lanes = (uint32_t)out_cols;
   m.lane_tiles = (m.lanes + kLanes - 1) / kLanes;
+  m.wide = host_aligned(d_out, 16) && out_stride * z % 16 == 0;
   uint64_t tiles;
   bool mapped;
   if (weights) {

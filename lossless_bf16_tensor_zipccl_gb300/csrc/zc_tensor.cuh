@@ -40,6 +40,44 @@ cudaError_t take_flag(const Word& word, cudaStream_t s, bool* ran_out) {
 }
 cudaError_t layer_waits(cudaStream_t s, bool* ran_out);  // zc_layer.cu
 
+// ---- pairs of blocks: two blocks of a cluster whose multiprocessors multiply
+// together.  The even one leads.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same place of another block's shared memory.
+__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  return a;
+}
+// Arrives once on a barrier of any block of the cluster.
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// As wait_phase, for what blocks of the cluster have arrived on.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(500000u)
+        : "memory");
+    if (done) return true;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    else if (now - t0 > kWaitLimitNs) return false;
+  }
+}
+
 // ---- tensor maps
 __device__ __forceinline__ void tma_prefetch(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -51,21 +89,30 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, int32_t 
       "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int32_t x, int32_t y, int32_t z, uint64_t* bar) {
+// Into this block's memory, announced at a barrier of either block of the pair.
+__device__ __forceinline__ void pair_load_2d(void* dst, const void* map, int32_t x, int32_t y, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
           smem_addr(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void pair_load_3d(void* dst, const void* map, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
 
-// ---- tensor memory: 128 lanes x 512 columns of 32 bits
+// ---- tensor memory: 128 lanes x 512 columns of 32 bits in each block of a pair;
+// both allocate and free
 __device__ __forceinline__ void tmem_alloc(uint32_t* at, uint32_t columns) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(columns) : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(columns) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
 }
 __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -84,9 +131,12 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&v)[32]) {
       : "memory");
 }
 
-// Arrives once on `bar` when the tensor operations that this thread has issued are done.
+// Arrives once on `bar` of both blocks of the pair when the tensor operations that
+// this thread has issued are done.
 __device__ __forceinline__ void tensor_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+               "h"((uint16_t)3)
+               : "memory");
 }
 
 // Descriptor of an operand in shared memory: lines of 128 bytes, their 16-byte
@@ -104,25 +154,26 @@ __device__ __forceinline__ uint64_t scale_operand(uint32_t smem) {
 }
 
 // 128 rows' scales into four columns of tensor memory: 32 lanes x 16 bytes, for
-// each of the four quarters of its lanes.
+// each of the four quarters of its lanes; in each block from its own memory.
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t from) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(from) : "memory");
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(from) : "memory");
 }
 
-// Instruction word of an E4M3 x E4M3 product of 128 x `columns`, E8M0 scales;
+// Instruction word of an E4M3 x E4M3 product of 256 x `columns`, E8M0 scales;
 // mn_a, mn_b: the operand lies across the sum.
 __device__ __forceinline__ uint32_t product_word(uint32_t columns, bool mn_a, bool mn_b) {
-  return (uint32_t)mn_a << 15 | (uint32_t)mn_b << 16 | (columns >> 3) << 17 | 1u << 23 | 1u << 27;
+  return (uint32_t)mn_a << 15 | (uint32_t)mn_b << 16 | (columns >> 3) << 17 | 1u << 23 | 1u << 28;
 }
 // The same with byte `i` of the scales' words.
 __device__ __forceinline__ uint32_t with_scale(uint32_t word, uint32_t i) { return word | i << 4 | i << 29; }
 
-// 32 places of the sum: tensor memory at d (+)= a x b.
+// 32 places of the sum: tensor memory at d (+)= a x b, in each block its 128 rows of
+// a; each has half the rows of b, and the scales of all.
 __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t word, uint32_t scale_a, uint32_t scale_b,
                                         bool add) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+      " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
       "l"(a), "l"(b), "r"(word), "r"(scale_a), "r"(scale_b), "r"((uint32_t)add)
       : "memory");
 }
