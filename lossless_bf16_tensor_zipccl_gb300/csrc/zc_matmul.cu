@@ -47,14 +47,14 @@ constexpr uint32_t kColumns = 256, kOwnColumns = 128, kPlaces = 128;  // columns
 constexpr uint32_t kStages = 5;
 constexpr uint32_t kBytesA = kOwnLanes * kPlaces, kBytesB = kOwnColumns * kPlaces, kStageBytes = kBytesA + kBytesB;
 constexpr uint32_t kScaleSets = 4, kScaleBytes = 512 * 3;  // four blocks' scales: 128 lanes, 256 columns
-constexpr uint32_t kBoxRows = 16;
+constexpr uint32_t kBoxRows = 16, kBoxes = 4;  // copies of 16, 32, 64 and 128 rows: as many as half a tile's columns need
 // Tensor memory: sums from columns 0 and 224 on, scales behind them, 16 columns for each of two sets.
 constexpr uint32_t kSecond = 224, kScaleColumns = kSecond + kColumns;
 
 __device__ unsigned int g_wait_ran_out;
 
 struct MatmulArgs {
-  CUtensorMap a, b;
+  CUtensorMap a, b[kBoxes];  // (WEIGHTS: b[0] alone)
   const uint8_t *scales_a, *scales_b;
   const int32_t* offsets;
   void* out;
@@ -65,6 +65,7 @@ struct MatmulArgs {
   uint32_t rows, chunks, lane_tiles, column_tiles;
   uint32_t b_blocks;                     // scales of a row
   bool wide;                             // rows of the result start at multiples of 16 bytes
+  bool whole_words;                      // scales of a row: whole words of four
 };
 
 struct Shared {
@@ -146,6 +147,48 @@ __device__ __forceinline__ void write_columns(const uint32_t (&v)[32], T* out, u
   }
 }
 
+// Scales of four blocks of the sum from k0 on, as tensor memory takes them: word j
+// of a lane is row 32 j + lane of the 128 lanes, then of the 256 columns, a byte for
+// each of the blocks.  What lies outside is read from inside: its rows are zeros or
+// not written, and no load hangs on a condition, which would make each wait for
+// the one before it (one set took 4,800 cycles so, the products of its blocks 2,048).
+template <bool kWeights>
+__device__ __forceinline__ void read_scales(const MatmulArgs& a, const Shared& s, const Tile& x, uint32_t k0, uint32_t (&w)[12]) {
+  const uint32_t lane = threadIdx.x % 32, last = x.blocks - 1;
+  if constexpr (kWeights) {
+    const uint64_t block = s.tiles[x.chunk];
+#pragma unroll
+    for (int j = 0; j < 12; ++j) {
+      const uint32_t wide = j < 4 ? a.lanes : a.columns;
+      const uint32_t at = min(j < 4 ? x.lane0 + 32 * j + lane : x.column0 + 32 * (j - 4) + lane, wide - 1);
+      const uint8_t* p = (j < 4 ? a.scales_a : a.scales_b) + block * wide + at;
+      uint32_t b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = __ldg(p + (uint64_t)min(k0 + i, last) * wide);
+      w[j] = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+    }
+  } else {
+    // a matrix's block of 128 x 128 has one scale for all lanes
+    const uint8_t* p = a.scales_a + x.chunk * a.a_matrix + (uint64_t)(min(x.lane0, a.lanes - 1) / kOwnLanes) * a.a_lane;
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __ldg(p + (uint64_t)min(k0 + i, last) * a.a_block);
+    w[0] = w[1] = w[2] = w[3] = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint8_t* q = a.scales_b + (uint64_t)(x.row + min(32 * j + lane, x.count - 1)) * a.b_blocks;
+      if (a.whole_words) {
+        w[4 + j] = __ldg(reinterpret_cast<const unsigned int*>(q + k0));
+      } else {
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = __ldg(q + min(k0 + i, last));
+        w[4 + j] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+      }
+    }
+  }
+}
+
 template <class T, int kForm>
 __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_constant__ MatmulArgs a) {
   constexpr bool kWeights = kForm == ZIPCCL_MATMUL_WEIGHTS;
@@ -156,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
   const uint32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   if (threadIdx.x == 0) {
     tma_prefetch(&a.a);
-    tma_prefetch(&a.b);
+    for (uint32_t i = 0; i < (kWeights ? 1 : kBoxes); ++i) tma_prefetch(&a.b[i]);
     for (uint32_t i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
     for (uint32_t i = 0; i < kScaleSets; ++i) mbar_init(&s.scales_full[i], 2), mbar_init(&s.scales_empty[i], 1);
     mbar_init(&s.clear, 1);
@@ -208,7 +251,6 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
       for (uint32_t t = pair; t < total && ok; t += pairs) {
         const Tile x = tile_of<kWeights>(a, s, t, rank);
         const uint32_t half = x.width / 2, column0 = x.column0 + rank * half;
-        const uint32_t pieces = kWeights ? 1 : half / kBoxRows;
         const uint32_t bytes = kBytesA + (kWeights ? kBytesB : half * kPlaces);
         for (uint32_t k = 0; k < x.blocks; ++k, ++n) {
           const uint32_t st = n % kStages;
@@ -222,9 +264,15 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
           else pair_load_3d(to, &a.a, x.lane0, x.row + at, 0, full);
           to += kBytesA;
           if constexpr (kWeights) {
-            pair_load_2d(to, &a.b, column0, x.row + at, full);
+            pair_load_2d(to, &a.b[0], column0, x.row + at, full);
           } else {
-            for (uint32_t i = 0; i < pieces; ++i) pair_load_2d(to + i * kBoxRows * kPlaces, &a.b, at, x.row + rank * half + i * kBoxRows, full);
+            uint32_t r = 0;
+#pragma unroll
+            for (int i = kBoxes - 1; i >= 0; --i)
+              if (half & kBoxRows << i) {
+                pair_load_2d(to + r * kPlaces, &a.b[i], at, x.row + rank * half + r, full);
+                r += kBoxRows << i;
+              }
           }
         }
       }
@@ -285,49 +333,36 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
       }
     }
   } else if (warp == 2) {
-    uint32_t sets = 0;
-    for (uint32_t t = pair; t < total && ok; t += pairs) {
-      const Tile x = tile_of<kWeights>(a, s, t, rank);
-      for (uint32_t k0 = 0; k0 < x.blocks; k0 += 4, ++sets) {
-        const uint32_t set = sets % kScaleSets, left = min(4u, x.blocks - k0);
-        // word j of a lane: row 32 j + lane, a byte for each of the four blocks
-        uint32_t w[12];
-#pragma unroll
-        for (int j = 0; j < 12; ++j) w[j] = 0;
-        if constexpr (kWeights) {
-          const uint64_t block = s.tiles[x.chunk] + k0;
-#pragma unroll
-          for (int j = 0; j < 12; ++j) {
-            const uint32_t at = j < 4 ? x.lane0 + 32 * j + lane : x.column0 + 32 * (j - 4) + lane;
-            const uint32_t wide = j < 4 ? a.lanes : a.columns;
-            const uint8_t* p = (j < 4 ? a.scales_a : a.scales_b) + block * wide + at;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (i < left && at < wide) w[j] |= (uint32_t)p[(uint64_t)i * wide] << (8 * i);
-          }
-        } else {
-          const uint8_t* p = a.scales_a + x.chunk * a.a_matrix + (uint64_t)(x.lane0 / kOwnLanes) * a.a_lane + (uint64_t)k0 * a.a_block;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < left && x.lane0 < a.lanes) w[0] |= (uint32_t)p[(uint64_t)i * a.a_block] << (8 * i);
-          w[1] = w[2] = w[3] = w[0];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t r = 32 * j + lane;
-            const uint8_t* q = a.scales_b + (uint64_t)(x.row + r) * a.b_blocks + k0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (i < left && r < x.count) w[4 + j] |= (uint32_t)q[i] << (8 * i);
-          }
-        }
-        if (!(ok = wait_cluster(&s.scales_empty[set], (sets / kScaleSets & 1) ^ 1))) break;
-        uint4* to = reinterpret_cast<uint4*>(s.scales[set]) + lane;
-#pragma unroll
-        for (int j = 0; j < 3; ++j) to[32 * j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive_at(at_rank(&s.scales_full[set], 0));
+    // a set is read while the one before it waits for its place
+    uint32_t sets = 0, t = pair, k0 = 0;
+    Tile x;
+    const auto next_tile = [&] {  // the next one with a sum, from t on
+      for (; t < total; t += pairs) {
+        x = tile_of<kWeights>(a, s, t, rank);
+        if (x.blocks) return;
       }
+    };
+    uint32_t w[12], later[12];
+    next_tile();
+    if (t < total) read_scales<kWeights>(a, s, x, k0, later);
+    while (t < total) {
+#pragma unroll
+      for (int j = 0; j < 12; ++j) w[j] = later[j];
+      if ((k0 += 4) >= x.blocks) {
+        k0 = 0;
+        t += pairs;
+        next_tile();
+      }
+      if (t < total) read_scales<kWeights>(a, s, x, k0, later);
+      const uint32_t set = sets % kScaleSets;
+      if (!(ok = wait_cluster(&s.scales_empty[set], (sets / kScaleSets & 1) ^ 1))) break;
+      uint4* to = reinterpret_cast<uint4*>(s.scales[set]) + lane;
+#pragma unroll
+      for (int j = 0; j < 3; ++j) to[32 * j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_at(at_rank(&s.scales_full[set], 0));
+      ++sets;
     }
   } else if (warp == 3) {
     if constexpr (kWeights) {
@@ -498,7 +533,7 @@ zipccl_status zipccl_moe_matmul(int form, const zipccl_fp8_blocks* a, const zipc
     m.scales_b = a->d_scales;
     m.columns = (uint32_t)outer;
     m.column_tiles = (m.columns + kColumns - 1) / kColumns;
-    mapped = code_map(&m.a, b, inner, rows, 1, 3, kPlaces) && code_map(&m.b, a, outer, rows, 1, 2, kPlaces);
+    mapped = code_map(&m.a, b, inner, rows, 1, 3, kPlaces) && code_map(&m.b[0], a, outer, rows, 1, 2, kPlaces);
     tiles = (uint64_t)experts * m.lane_tiles * m.column_tiles;
   } else {
     const uint32_t high = (uint32_t)((outer + kFp8Block - 1) / kFp8Block), wide = (uint32_t)((inner + kFp8Block - 1) / kFp8Block);
@@ -510,7 +545,9 @@ zipccl_status zipccl_moe_matmul(int form, const zipccl_fp8_blocks* a, const zipc
     m.a_block = forward ? 1 : wide;
     m.sum = (uint32_t)(forward ? inner : outer);
     m.b_blocks = forward ? wide : high;
-    mapped = code_map(&m.a, b, inner, outer, experts, 3, kPlaces) && code_map(&m.b, a, m.sum, rows, 1, 2, kBoxRows);
+    m.whole_words = m.b_blocks % 4 == 0 && host_aligned(a->d_scales, 4);
+    mapped = code_map(&m.a, b, inner, outer, experts, 3, kOwnLanes);
+    for (uint32_t i = 0; i < kBoxes; ++i) mapped = mapped && code_map(&m.b[i], a, m.sum, rows, 1, 2, kBoxRows << i);
     tiles = (rows / kColumns + experts + 1) * m.lane_tiles;  // at most
   }
   if (!mapped) return ZIPCCL_ERR_CUDA;
