@@ -24,7 +24,7 @@
 // The weights are read along the sum forward and across it backward, from the
 // same codes: blocks of 128 x 128 serve both.
 //
-// Warps: 0 loads tiles through tensor maps, five stages of 128 places ahead; 1 (of
+// Warps: 0 loads tiles through tensor maps, six stages of 128 places ahead; 1 (of
 // the leading block) issues the products; 2 lays the scales out (128 rows x 4
 // bytes, four blocks of the sum a time); 3 clears what a chunk's last block of rows
 // reads of the next chunk (gradient of the weights); 4 to 11 write results.
@@ -44,7 +44,7 @@ namespace {
 constexpr int kWriters = 8, kThreads = (4 + kWriters) * 32;
 constexpr uint32_t kLanes = 256, kOwnLanes = 128;                   // of a tile, and those of a block
 constexpr uint32_t kColumns = 256, kOwnColumns = 128, kPlaces = 128;  // columns; places of the sum in a stage
-constexpr uint32_t kStages = 5;
+constexpr uint32_t kStages = 6;
 constexpr uint32_t kBytesA = kOwnLanes * kPlaces, kBytesB = kOwnColumns * kPlaces, kStageBytes = kBytesA + kBytesB;
 constexpr uint32_t kScaleSets = 4, kScaleBytes = 512 * 3;  // four blocks' scales: 128 lanes, 256 columns
 constexpr uint32_t kBoxRows = 16, kBoxes = 4;  // copies of 16, 32, 64 and 128 rows: as many as half a tile's columns need
@@ -71,8 +71,9 @@ struct MatmulArgs {
 struct Shared {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
   alignas(128) uint8_t scales[kScaleSets][kScaleBytes];
-  alignas(16) uint8_t turned[kWriters][32 * 32 * 4];  // results of a writing warp, the other way round
-  uint64_t full[kStages], empty[kStages], scales_full[kScaleSets], scales_empty[kScaleSets], clear, cleared;
+  alignas(16) uint8_t turned[kWriters][32 * 64];  // 16-bit results of a writing warp, the other way round
+  uint64_t full[kStages], empty[kStages], scales_full[kScaleSets], scales_empty[kScaleSets];
+  uint64_t ends[kStages], clear[kStages], cleared[kStages];  // a stage with a chunk's last block (gradient of the weights)
   uint64_t done[2], shared_taken[2], taken[2];
   uint32_t tmem;
   uint32_t first[kMaxChunks + 2];  // first row of each chunk; the rows behind the last are one more
@@ -120,31 +121,47 @@ __device__ __forceinline__ Tile tile_of(const MatmulArgs& a, const Shared& s, ui
   return x;
 }
 
-// 32 columns of a warp's 32 lanes, from column c of `count`: out + column * stride
-// + lane.  Where rows are wide they are turned in shared memory first, so that a
-// warp writes 16 bytes a lane, 64 or 128 consecutive ones; `lanes`: those in range.
 template <class T>
-__device__ __forceinline__ void write_columns(const uint32_t (&v)[32], T* out, uint64_t stride, uint32_t c, uint32_t count, uint32_t lanes,
-                                              bool wide, uint8_t* turned) {
-  const uint32_t lane = threadIdx.x % 32;
-  if (wide && lanes >= 32) {
-    T* s = reinterpret_cast<T*>(turned);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s[i * 32 + lane] = from_float<T>(__uint_as_float(v[i]));
-    __syncwarp();
-    constexpr uint32_t kPer = 16 / sizeof(T), kAcross = 32 / kPer;  // values of a lane, lanes of a row
-#pragma unroll
-    for (uint32_t i = 0; i < 32; i += 32 / kAcross) {
-      const uint32_t row = i + lane / kAcross, at = lane % kAcross * kPer;
-      const uint4 q = *reinterpret_cast<const uint4*>(s + row * 32 + at);
-      if (c + row < count) *reinterpret_cast<uint4*>(out + (c + row) * stride + at) = q;
-    }
-    __syncwarp();
-  } else if (lane < lanes) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (c + i < count) out[(c + i) * stride + lane] = from_float<T>(__uint_as_float(v[i]));
+__device__ __forceinline__ uint32_t pair_of(uint32_t a, uint32_t b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(__uint_as_float(a), __uint_as_float(b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(a), __uint_as_float(b));
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
+}
+
+// Results of 16 bits: 32 columns of a warp's 32 lanes go to shared memory the other
+// way round (four instructions; value by value it took 32, and the writing warps
+// held the gradient of the weights at twice its time) and from there in 16 bytes a
+// lane, 64 consecutive ones of a column: from column c of `count` to out + column *
+// stride.  The pieces of a column lie at other places in every second line, so
+// that neither access meets itself in a bank.
+template <class T>
+__device__ __forceinline__ void turn_columns(const uint32_t (&v)[2][16], uint8_t* turned) {
+  const uint32_t lane = threadIdx.x % 32, matrix = lane / 8, base = smem_addr(turned);
+#pragma unroll
+  for (uint32_t h = 0; h < 2; ++h)
+#pragma unroll
+    for (uint32_t q = 0; q < 2; ++q) {
+      const uint32_t line = (2 * q + matrix / 2) * 8 + lane % 8, piece = (2 * h + matrix % 2) ^ (line / 2 % 4);
+      const uint32_t(&x)[16] = v[h];
+      store_turned(base + line * 64 + piece * 16, pair_of<T>(x[8 * q], x[8 * q + 1]), pair_of<T>(x[8 * q + 2], x[8 * q + 3]),
+                   pair_of<T>(x[8 * q + 4], x[8 * q + 5]), pair_of<T>(x[8 * q + 6], x[8 * q + 7]));
+    }
+  __syncwarp();
+}
+template <class T>
+__device__ __forceinline__ void write_turned(const uint8_t* turned, T* out, uint64_t stride, uint32_t c, uint32_t count) {
+  const uint32_t lane = threadIdx.x % 32;
+#pragma unroll
+  for (uint32_t i = 0; i < 32; i += 8) {
+    const uint32_t line = i + lane / 4, piece = lane % 4 ^ (line / 2 % 4);
+    const uint4 q = *reinterpret_cast<const uint4*>(turned + line * 64 + piece * 16);
+    if (c + line < count) *reinterpret_cast<uint4*>(out + (c + line) * stride + lane % 4 * 8) = q;
+  }
+  __syncwarp();
 }
 
 // Scales of four blocks of the sum from k0 on, as tensor memory takes them: word j
@@ -202,8 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
     for (uint32_t i = 0; i < (kWeights ? 1 : kBoxes); ++i) tma_prefetch(&a.b[i]);
     for (uint32_t i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1), mbar_init(&s.empty[i], 1);
     for (uint32_t i = 0; i < kScaleSets; ++i) mbar_init(&s.scales_full[i], 2), mbar_init(&s.scales_empty[i], 1);
-    mbar_init(&s.clear, 1);
-    mbar_init(&s.cleared, 2);
+    for (uint32_t i = 0; i < kStages; ++i) mbar_init(&s.ends[i], 1), mbar_init(&s.clear[i], 1), mbar_init(&s.cleared[i], 2);
     for (uint32_t i = 0; i < 2; ++i) mbar_init(&s.done[i], 1), mbar_init(&s.shared_taken[i], 2 * kWriters), mbar_init(&s.taken[i], 2 * kWriters);
   }
   if (warp == 1) tmem_alloc(&s.tmem, 512);
@@ -265,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
           to += kBytesA;
           if constexpr (kWeights) {
             pair_load_2d(to, &a.b[0], column0, x.row + at, full);
+            if (rank == 0 && k + 1 == x.blocks && x.count % 32) mbar_arrive(&s.ends[st]);
           } else {
             uint32_t r = 0;
 #pragma unroll
@@ -281,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      uint32_t n = 0, sets = 0, tiles = 0, clears = 0, columns = 0;
+      uint32_t n = 0, sets = 0, tiles = 0, columns = 0, cleared = 0;  // cleared: a parity for each stage
       for (uint32_t t = pair; t < total && ok; t += pairs) {
         const Tile x = tile_of<kWeights>(a, s, t, rank);
         if (x.blocks == 0) continue;
@@ -314,10 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
           if (kWeights && k + 1 == x.blocks && x.count % kPlaces) {
             steps = (x.count % kPlaces + 31) / 32;
             if (x.count % 32) {
-              arrive_at(at_rank(&s.clear, 0));
-              arrive_at(at_rank(&s.clear, 1));
-              if (!(ok = wait_cluster(&s.cleared, clears & 1))) break;
-              ++clears;
+              if (!(ok = wait_cluster(&s.cleared[st], cleared >> st & 1))) break;
+              cleared ^= 1u << st;
             }
           }
           tmem_fence_after();
@@ -366,22 +381,30 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
     }
   } else if (warp == 3) {
     if constexpr (kWeights) {
-      uint32_t n = 0, clears = 0;
+      // The leading block's loading thread says that a chunk's last block is on its way
+      // (so that the barrier of its stage is at that turn), this warp of the leading
+      // block sees it arrive and tells the other's; both clear their half, before the
+      // products come to it.
+      uint32_t n = 0, parity = 0;  // parity: a bit for each stage
       for (uint32_t t = pair; t < total && ok; t += pairs) {
         const Tile x = tile_of<kWeights>(a, s, t, rank);
         n += x.blocks;
         if (x.count % 32 == 0) continue;
-        // the leading block's warp 1 asks for it when the stage has arrived in both, and goes on when it is done
-        if (!(ok = wait_cluster(&s.clear, clears & 1))) break;
-        ++clears;
         const uint32_t st = (n - 1) % kStages, from = x.count % kPlaces, upto = (from + 31) / 32 * 32;
+        if (rank == 0) {
+          if (!(ok = wait_phase(&s.ends[st], parity >> st & 1)) || !(ok = wait_cluster(&s.full[st], (n - 1) / kStages & 1))) break;
+          if (lane == 0) arrive_at(at_rank(&s.clear[st], 1));
+        } else if (!(ok = wait_cluster(&s.clear[st], parity >> st & 1))) {
+          break;
+        }
+        parity ^= 1u << st;
         for (uint32_t i = from * 8 + lane; i < upto * 8; i += 32)
 #pragma unroll
           for (int piece = 0; piece < 2; ++piece)
             reinterpret_cast<uint4*>(s.stage[st] + piece * kBytesA)[i] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_at(at_rank(&s.cleared, 0));
+        if (lane == 0) arrive_at(at_rank(&s.cleared[st], 0));
       }
     }
   } else {
@@ -401,34 +424,49 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
         if (!(ok = wait_cluster(&s.done[buffer], (tiles >> 1) & 1))) break;
         tmem_fence_after();
       }
-      bool told = false;
       const uint32_t parts = x.width / 32;
       // (backwards in the first buffer)
       for (uint32_t i = other; i < parts + other; i += 2) {
         const bool mine = i < parts;
         const uint32_t c = (buffer ? i : parts - 1 - i) * 32;
-        uint32_t v[32];
-        if (mine && x.blocks) {
-          tmem_load32(sums + c, v);
-          tmem_wait_load();
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0;
-        }
-        if (x.blocks && !told) {
-          told = true;
+        const auto given_back = [&] {  // tensor memory, before the results are written
           tmem_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_at(at_rank(&s.shared_taken[buffer], 0));
+          if (lane == 0 && i == other) arrive_at_relaxed(at_rank(&s.shared_taken[buffer], 0));
+          if (lane == 0 && i + 2 >= parts + other) arrive_at_relaxed(at_rank(&s.taken[buffer], 0));
+        };
+        if (sizeof(T) == 2 && a.wide && lanes >= 32 && x.blocks) {
+          if constexpr (sizeof(T) == 2) {
+            uint32_t v[2][16];
+            if (mine) {
+              tmem_load_16x32(sums + c, v[0]);
+              tmem_load_16x32(sums + (16u << 16) + c, v[1]);
+              tmem_wait_load();
+            }
+            given_back();
+            if (mine) {
+              turn_columns<T>(v, s.turned[warp - 4]);
+              write_turned<T>(s.turned[warp - 4], out, a.out_stride, c, x.columns);
+            }
+          }
+        } else {
+          uint32_t v[32];
+          if (mine && x.blocks) {
+            tmem_load32(sums + c, v);
+            tmem_wait_load();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0;
+          }
+          if (x.blocks) given_back();
+          if (mine && lane < lanes) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < x.columns) out[(c + j) * a.out_stride + lane] = from_float<T>(__uint_as_float(v[j]));
+          }
         }
-        if (mine) write_columns<T>(v, out, a.out_stride, c, x.columns, lanes, a.wide, s.turned[warp - 4]);
       }
-      if (x.blocks) {
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_at(at_rank(&s.taken[buffer], 0));
-        ++tiles;
-      }
+      tiles += x.blocks != 0;
     }
   }
   if (!ok) atomicOr(&g_wait_ran_out, 1u);

@@ -61,6 +61,11 @@ __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same without waiting for this thread's earlier stores: for what it has read
+// from tensor memory (after tmem_wait_load and tmem_fence_before).
+__device__ __forceinline__ void arrive_at_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // As wait_phase, for what blocks of the cluster have arrived on.
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
   uint64_t t0 = 0;
@@ -137,6 +142,24 @@ __device__ __forceinline__ void tensor_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
                "h"((uint16_t)3)
                : "memory");
+}
+
+// 32 columns of 16 lanes, in the order of a matrix instruction's result: of each 8
+// columns a lane of the warp has columns 2 (lane % 4) and + 1 of rows lane / 4 and
+// lane / 4 + 8.
+__device__ __forceinline__ void tmem_load_16x32(uint32_t at, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(at)
+      : "memory");
+}
+// Four 8 x 8 matrices of 16-bit values in that order, the other way round: a
+// column's 8 values become 16 consecutive bytes.  Lane l has the place of column
+// l % 8 of matrix l / 8.
+__device__ __forceinline__ void store_turned(uint32_t at, uint32_t m0, uint32_t m1, uint32_t m2, uint32_t m3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(m0), "r"(m1), "r"(m2), "r"(m3) : "memory");
 }
 
 // Descriptor of an operand in shared memory: lines of 128 bytes, their 16-byte
