@@ -17,9 +17,10 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libzipccl.so")
 SOURCES = ["zc_api.cu", "zc_encode.cu", "zc_decode.cu", "zc_noalloc.cu", "zc_codebook.cpp", "zc_route.cu",
-           "zc_dispatch.cu", "zc_adamw.cu", "zc_quantize.cu", "zc_matmul.cu", "zc_layer.cu"]
+           "zc_dispatch.cu", "zc_adamw.cu", "zc_quantize.cu", "zc_matmul.cu", "zc_layer_up.cu",
+           "zc_layer_down.cu"]
 HEADERS = ["zc_format.h", "zc_device.cuh", "zc_kernels.h", "zc_codebook.h", "zc_ops.cuh", "zc_fp8.cuh",
-           "zc_tensor.cuh", "zc_route.cuh"]
+           "zc_tensor.cuh", "zc_route.cuh", "zc_layer.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # No fast-math: the reduce folds in IEEE fp32 with subnormals kept.
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-ftz=false", "-prec-div=true",

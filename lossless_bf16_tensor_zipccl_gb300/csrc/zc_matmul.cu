@@ -39,6 +39,10 @@
 #include "zipccl.h"
 
 namespace zc {
+
+cudaError_t layer_up_waits(cudaStream_t s, bool* ran_out);    // zc_layer_up.cu
+cudaError_t layer_down_waits(cudaStream_t s, bool* ran_out);  // zc_layer_down.cu
+
 namespace {
 
 constexpr int kWriters = 8, kThreads = (4 + kWriters) * 32;
@@ -599,7 +603,8 @@ zipccl_status zipccl_moe_matmul(int form, const zipccl_fp8_blocks* a, const zipc
 zipccl_status zipccl_moe_status(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   bool ran_out = false;
-  if (take_flag(g_wait_ran_out, s, &ran_out) != cudaSuccess || layer_waits(s, &ran_out) != cudaSuccess) return ZIPCCL_ERR_CUDA;
+  if (take_flag(g_wait_ran_out, s, &ran_out) != cudaSuccess || layer_up_waits(s, &ran_out) != cudaSuccess ||
+      layer_down_waits(s, &ran_out) != cudaSuccess) return ZIPCCL_ERR_CUDA;
   return ran_out ? ZIPCCL_ERR_TIMEOUT : ZIPCCL_OK;
 }
 

@@ -38,7 +38,6 @@ cudaError_t take_flag(const Word& word, cudaStream_t s, bool* ran_out) {
   }
   return e;
 }
-cudaError_t layer_waits(cudaStream_t s, bool* ran_out);  // zc_layer.cu
 
 // ---- pairs of blocks: two blocks of a cluster whose multiprocessors multiply
 // together.  The even one leads.
