@@ -504,16 +504,13 @@ struct Stages {
 __device__ __forceinline__ void warps_sync(uint32_t id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void warps_arrive(uint32_t id) { asm volatile("bar.arrive %0, 256;" ::"r"(id) : "memory"); }
 
-// ---- what both kernels know of the pairs: the active experts in order, their
-// tokens, where each one's pairs begin, each pair's token and weight
+// ---- what both kernels know of the pairs: the active experts in order, where each
+// one's pairs begin, each pair's token and weight
 template <int G>
 struct Pairs {
   static constexpr uint32_t N = 8 * G * kMaxTopK;
   uint32_t count;  // active experts
-  union {
-    uint32_t tokens[N];  // second kernel: a bit for each token of an active expert
-    float weight[N];     // first kernel: of each pair
-  };
+  float weight[N];  // of each pair (first kernel)
   uint16_t expert[N];
   uint16_t begin[N + 1];
   uint8_t token[N];
@@ -546,7 +543,6 @@ __device__ __forceinline__ void gather_pairs(Pairs<G>& p, PairSource& s, uint32_
       if (n) {
         const uint32_t a = active + __popc(who & ((1u << lane) - 1));
         p.expert[a] = (uint16_t)e;
-        if constexpr (!kWeights) p.tokens[a] = mask;
         p.begin[a] = (uint16_t)(upto - n);
       }
       active += __popc(who);

@@ -9,10 +9,9 @@ __device__ unsigned int g_layer_down_ran_out;
 
 // 16 hidden places at a time; the pieces of the active experts' rows, one expert
 // after the other, are dealt out in equal runs to 1, 2, 4 or 8 blocks of a cluster:
-// whichever leaves the fewest pieces to the block that has most.  With one group of
-// tokens the columns are the tokens themselves, so that a tile's sums stay in
-// registers over all experts; with more, a warp adds what an expert gives to its
-// tokens' sums in shared memory.  A block adds its warps', and after 8 tiles the
+// whichever leaves the fewest pieces to the block that has most.  A warp adds what an
+// expert gives to its tokens' sums in shared memory: an expert's columns are its own
+// tokens only, so that nothing of it reaches another's.  A block adds its warps', and after 8 tiles the
 // blocks that share them each all blocks' of some of them.
 template <bool kShift, class T, class W, int G>
 __device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs<G>& pairs, Ring& ring, uint8_t* memory) {
@@ -25,7 +24,7 @@ __device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs<G>& p
   float* own = warps + warp * size;        // a warp's sums
   float* block = warps + kWarps * size;    // a block's, of a round's tiles
   const auto* h = static_cast<const typename X::Value*>(a.h);
-  const uint64_t apart = (uint64_t)(a.tokens * a.top_k + 1) * a.h_stride;
+  const uint64_t apart = (uint64_t)a.tokens * a.top_k * a.h_stride;
   // whole chunks of a row, and their pieces (one at least); what is left is a warp's of the block that has a row's last
   const uint32_t body = a.inner / kPlacesOfChunk<W> * kPlacesOfChunk<W>, pieces = max((body + kPlacesOfPiece<W> - 1) / kPlacesOfPiece<W>, 1u);
   const uint32_t all = pieces * pairs.count;
@@ -64,12 +63,7 @@ __device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs<G>& p
   const uint32_t k0 = warp * kPlacesOfChunk<W>;
   const auto vector = [&](uint32_t n, uint32_t col) -> const typename X::Value* {  // of a column of active expert n
     uint32_t at = pairs.begin[n] + col;
-    if constexpr (G == 1) {
-      const uint32_t mask = pairs.tokens[n];
-      at = mask >> col & 1 ? pairs.begin[n] + __popc(mask & ((1u << col) - 1)) : a.tokens * a.top_k;
-    } else if (at >= pairs.begin[n + 1]) {
-      at = a.tokens * a.top_k;
-    }
+    if (at >= pairs.begin[n + 1]) at = pairs.begin[n];  // (not used)
     return h + (uint64_t)at * a.h_stride;
   };
   Chunk<W, X, false> x[2];
@@ -81,15 +75,13 @@ __device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs<G>& p
       if (tile >= tiles) break;
       const uint32_t r0 = min(tile * 16 + gid, a.hidden - 1), r1 = min(tile * 16 + gid + 8, a.hidden - 1);
       float c[G][4] = {};
-      if constexpr (G > 1) {
-        for (uint32_t i = lane; i < size; i += 32) own[i] = 0.0f;
-        __syncwarp();
-      }
+      for (uint32_t i = lane; i < size; i += 32) own[i] = 0.0f;
+      __syncwarp();
       uint32_t n = from / pieces, p = from - n * pieces;
       for (uint32_t s = from; s < upto;) {  // an expert's pieces of the run
         const uint32_t begin = pairs.begin[n], tokens = pairs.begin[n + 1] - begin;
         Vectors<X, G> v;
-        v.apart = apart, v.groups = G == 1 ? 1 : (tokens + 7) / 8;
+        v.apart = apart, v.groups = (tokens + 7) / 8;
 #pragma unroll
         for (int g = 0; g < G; ++g) v.v[g] = vector(n, g * 8 + gid);
         const W* at = static_cast<const W*>(a.down) + (uint64_t)pairs.expert[n] * a.hidden * a.down_stride;
@@ -118,24 +110,17 @@ __device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs<G>& p
           take_chunk<true, kShift, false, W, X, G>(c, nullptr, its, v, x[1], body, a.inner);
         }
         p = 0, ++n;
-        if constexpr (G > 1) {
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            if (g >= (int)v.groups) break;
+        for (int g = 0; g < G; ++g) {
+          if (g >= (int)v.groups) break;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t col = g * 8 + quad * 2 + i % 2;
-              if (col < tokens) own[pairs.token[begin + col] * 16 + gid + (i / 2) * 8] += c[g][i];
-              c[g][i] = 0.0f;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t col = g * 8 + quad * 2 + i % 2;
+            if (col < tokens) own[pairs.token[begin + col] * 16 + gid + (i / 2) * 8] += c[g][i];
+            c[g][i] = 0.0f;
           }
-          __syncwarp();
         }
-      }
-      if constexpr (G == 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (quad * 2 + i % 2 < a.tokens) own[(quad * 2 + i % 2) * 16 + gid + (i / 2) * 8] = c[0][i];
+        __syncwarp();
       }
       __syncthreads();
       for (uint32_t i = threadIdx.x; i < size; i += kThreads) {
@@ -225,8 +210,7 @@ extern "C" {
 
 zipccl_status zipccl_moe_layer_workspace_bytes(uint64_t tokens, uint32_t top_k, uint64_t inner, uint64_t* out_bytes) {
   if (!out_bytes || tokens > kMaxTokens || top_k == 0 || top_k > kMaxTopK || inner >= (1ull << 22)) return ZIPCCL_ERR_INVALID_ARG;
-  // a row for each pair and one of zeros, two floats or three bfloat16 a value
-  *out_bytes = ((tokens * top_k + 1) * ((inner + 7) / 8 * 8) * 8 + 255) / 256 * 256;
+  *out_bytes = (tokens * top_k * ((inner + 7) / 8 * 8) * 8 + 255) / 256 * 256;  // two floats or three bfloat16 a value
   return ZIPCCL_OK;
 }
 

@@ -118,7 +118,7 @@ __device__ __forceinline__ void layer_up(const LayerArgs& a, const Pairs<G>& pai
   const Matrix matrix = {&a.up_map, static_cast<const uint8_t*>(a.up), (uint64_t)a.experts * rows, a.up_stride * sizeof(W), a.hidden * (uint32_t)sizeof(W)};
   Stages<kStages, kShiftW, Fill> stages(ring, memory, matrix, fill, &g_layer_up_ran_out);
   float4* sums = reinterpret_cast<float4*>(memory + kStages * kStageBytes<kShiftW>);
-  const uint64_t apart = (uint64_t)(a.tokens * a.top_k + 1) * a.h_stride;
+  const uint64_t apart = (uint64_t)a.tokens * a.top_k * a.h_stride;
   const uint32_t k0 = warp * kPlacesOfChunk<W>;
   const auto vector = [&](uint32_t n, uint32_t col) -> const T* {  // of the column of active expert n
     uint32_t at = pairs.begin[n] + col;
@@ -245,12 +245,6 @@ __global__ void __launch_bounds__(kThreads, 2) zc_layer_up_kernel(const __grid_c
   }
   cluster_sync();  // also: nobody reads this block's shared memory any more
   gather_pairs<true>(s_pairs, source, a.tokens, a.top_k, a.experts);
-  // the rows of h that columns without a token read in the second kernel
-  if (blockIdx.x == 0) {
-    auto* zero = static_cast<typename PartsFor<W>::Value*>(a.h) + (uint64_t)a.tokens * a.top_k * a.h_stride;
-    const uint64_t apart = (uint64_t)(a.tokens * a.top_k + 1) * a.h_stride;
-    for (uint32_t i = threadIdx.x; i < a.inner; i += kThreads) store_parts(zero + i, apart, 0.0f);
-  }
   layer_up<kShift, T, W, G>(a, s_pairs, s_ring, s_dyn);
 }
 

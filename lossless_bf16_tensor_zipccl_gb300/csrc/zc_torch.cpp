@@ -466,6 +466,7 @@ Blocks blocks(PyObject* o, const char* what) {
 // Bytes between rows of codes [.., rows, cols], whose matrices lie rows apart.
 uint64_t code_stride(const Tensor& t, const char* what) {
   const int64_t d = t.dim(), rows = t.size(d - 2), cols = t.size(d - 1);
+  if (t.numel() == 0) return (uint64_t)((cols + 15) / 16 * 16);
   const bool apart = rows > 1 || (d == 3 && t.size(0) > 1);
   const int64_t stride = rows > 1 ? t.stride(d - 2) : d == 3 && t.size(0) > 1 ? t.stride(0) : (cols + 15) / 16 * 16;
   if (!t.is_cuda() || (cols > 1 && t.stride(d - 1) != 1) || (apart && (stride % 16 || stride < cols)) ||
