@@ -54,10 +54,11 @@ template <bool kShift>
 constexpr uint32_t kPitch = kPiece + (kShift ? 64 : 0);
 template <bool kShift>
 constexpr uint32_t kStageBytes = 16 * kPitch<kShift>;
-// stages of a block: what two blocks of a multiprocessor have room for
-template <int G>
-constexpr uint32_t kStagesOf = G == 1 ? 3 : 2;
 constexpr uint32_t kMaxStages = 3;
+// Shared memory that leaves room for two blocks of a multiprocessor, without what
+// the kernels declare themselves.
+constexpr size_t kRoomForTwo = 114000;
+constexpr uint32_t kTokens = 8;  // columns of an instruction: tokens of an expert taken together
 
 struct LayerArgs {
   CUtensorMap up_map, down_map;  // 8 rows x 256 words of 8 bytes
@@ -68,7 +69,7 @@ struct LayerArgs {
   int32_t* ids;
   void* h;  // parts of each pair's inner places, rows of h_stride values
   uint64_t x_stride, up_stride, down_stride, h_stride;  // in values
-  uint32_t tokens, hidden, inner, experts, top_k;
+  uint32_t tokens, hidden, inner, experts, top_k, stages;
   int activation;
   bool gated, router_float;
   bool shift_up, shift_down;  // rows start anywhere (up: of up, x or router)
@@ -82,6 +83,19 @@ __device__ __forceinline__ float load_cluster(uint32_t a) {
 }
 __device__ __forceinline__ void store_cluster(uint32_t a, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// Sum over blocks first .. first + count - 1 of the cluster of one place of their shared memory, in order;
+// all are asked for before the first is used (one after the other they take a
+// quarter of a microsecond each).
+__device__ __forceinline__ float cluster_sum(const float* p, uint32_t first, uint32_t count) {
+  float v[kCluster], sum = 0.0f;
+#pragma unroll
+  for (uint32_t r = 0; r < kCluster; ++r) v[r] = load_cluster(at_rank(p, first + min(r, count - 1)));
+#pragma unroll
+  for (uint32_t r = 0; r < kCluster; ++r)
+    if (r < count) sum += v[r];
+  return sum;
 }
 
 // ---- values
@@ -202,25 +216,27 @@ __device__ __forceinline__ uint4 keep(uint4 q, int left) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// h as the second kernel takes it, each part in an array of its own: with bfloat16
-// weights three bfloat16 values (24 bits), with others two floats of 11 bits.
-struct ThreeParts {
+// h as the second kernel takes it, each part in an array of its own.  Where the
+// layer's type has 16 bits two bfloat16 values: 16 bits, 2^-17 of h off at most,
+// where the result's own rounding is 2^-9 or 2^-12; half the loads of two floats and
+// two thirds of the products of three.  For 32-bit layers two floats of 11 bits.
+struct TwoSmall {
   using Value = __nv_bfloat16;
-  static constexpr int kParts = 3;
+  static constexpr int kParts = 2;
 };
 struct TwoParts {
   using Value = float;
   static constexpr int kParts = 2;
 };
-template <class W>
-using PartsFor = std::conditional_t<std::is_same<W, __nv_bfloat16>::value, ThreeParts, TwoParts>;
+template <class T>
+using PartsFor = std::conditional_t<sizeof(T) == 2, TwoSmall, TwoParts>;
 template <class X>
 struct PartsOf {  // of a plain vector: itself
   using Value = X;
   static constexpr int kParts = 1;
 };
 template <>
-struct PartsOf<ThreeParts> : ThreeParts {};
+struct PartsOf<TwoSmall> : TwoSmall {};
 template <>
 struct PartsOf<TwoParts> : TwoParts {};
 
@@ -229,12 +245,11 @@ __device__ __forceinline__ float bf16_part(float v) {
   if (isinf(p) && !isinf(v)) p = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
   return p;
 }
-// Writes the parts of v to at[0], at[apart], ...
+// Writes the parts of v to at[0] and at[apart].
 __device__ __forceinline__ void store_parts(__nv_bfloat16* at, uint64_t apart, float v) {
-  const float p = bf16_part(v), r = isfinite(v) ? v - p : 0.0f, q = bf16_part(r);
+  const float p = bf16_part(v);
   at[0] = __float2bfloat16_rn(p);
-  at[apart] = __float2bfloat16_rn(q);
-  at[2 * apart] = __float2bfloat16_rn(r - q);
+  at[apart] = __float2bfloat16_rn(isfinite(v) ? v - p : 0.0f);
 }
 __device__ __forceinline__ void store_parts(float* at, uint64_t apart, float v) {
   float hi, lo;
@@ -331,13 +346,12 @@ __device__ __forceinline__ void step_products(float (&t)[4], const uint4& w0, co
   }
 }
 
-// Where the vectors of a product's columns lie: v[g], that of column gid of group
-// g; a column without a token has another's.
-template <class X, int G>
-struct Vectors {
-  const typename PartsOf<X>::Value* v[G];
-  uint64_t apart;  // to a vector's next part
-  uint32_t groups;
+// Where the vector of a lane's column lies (gid's; a column without a token has
+// another's, and its sums are not used), and its next part.
+template <class X>
+struct Vector {
+  const typename PartsOf<X>::Value* at;
+  uint64_t apart;
 };
 
 // What a warp reads of the matrices: rows gid and gid + 8 of 16, and their scales.
@@ -347,12 +361,12 @@ struct Rows {
   const uint8_t *scale0, *scale1;
 };
 
-// The first group's vectors for a chunk, or for one step of it where a lane's share
+// The vectors for a chunk, or for one step of it where a lane's share
 // of two would take too many registers.
 template <class W, class X, bool kShift>
 struct Chunk {
   using R = RawShare<W, X, kShift>;
-  static constexpr bool kBothSteps = 2 * sizeof(R) <= 128;
+  static constexpr bool kBothSteps = 2 * sizeof(R) <= 64;
   R x[kBothSteps ? 2 : 1];
   __device__ __forceinline__ void load(const typename R::Value* p, uint64_t apart, uint32_t k0, uint32_t n) {
     const uint32_t k = k0 + threadIdx.x % 4 * kPer16<W>;
@@ -361,14 +375,14 @@ struct Chunk {
   }
 };
 
-// A warp's chunk of 16 rows at place k0 of n, times G groups of 8 vectors; `first`:
-// the first group's.  stage: the lane's share of the chunk in shared memory (row
-// gid, its first 16 bytes); kTail: the chunk is not whole, and read in place.  The
-// sums of a chunk begin at 0 and are added to c here.  8-bit weights: the places of
-// a chunk are a block.  kShiftW, kShiftX: rows, vectors may start anywhere.
-template <bool kTail, bool kShiftW, bool kShiftX, class W, class X, int G>
-__device__ __forceinline__ void take_chunk(float (&c)[G][4], const uint8_t* stage, const Rows<W>& rows, const Vectors<X, G>& x,
-                                           Chunk<W, X, kShiftX>& first, uint32_t k0, uint32_t n) {
+// A warp's chunk of 16 rows at place k0 of n, times 8 vectors, those in `mine`.
+// stage: the lane's share of the chunk in shared memory (row gid, its first 16
+// bytes); kTail: the chunk is not whole, and read in place.  The sums of a chunk
+// begin at 0 and are added to c here.  8-bit weights: the places of a chunk are a
+// block.  kShiftW, kShiftX: rows, vectors may start anywhere.
+template <bool kTail, bool kShiftW, bool kShiftX, class W, class X>
+__device__ __forceinline__ void take_chunk(float (&c)[4], const uint8_t* stage, const Rows<W>& rows, const Vector<X>& x,
+                                           Chunk<W, X, kShiftX>& mine, uint32_t k0, uint32_t n) {
   constexpr uint32_t S = kStep<W>;
   using C = Chunk<W, X, kShiftX>;
   const uint32_t k = k0 + threadIdx.x % 4 * kPer16<W>;
@@ -398,19 +412,14 @@ __device__ __forceinline__ void take_chunk(float (&c)[G][4], const uint8_t* stag
       w0[u] = keep<W>(w0[u], left), w1[u] = keep<W>(w1[u], left);
     }
   }
+  float t[4] = {};
+  step_products<W, X>(t, w0[0], w1[0], mine.x[0].used(x.at, k, n, !kTail));
+  if constexpr (!C::kBothSteps) mine.x[0].load(x.at, x.apart, k + S, n);
+  step_products<W, X>(t, w0[1], w1[1], mine.x[C::kBothSteps ? 1 : 0].used(x.at, k + S, n, !kTail));
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    if (g >= (int)x.groups) break;
-    if (g) first.load(x.v[g], x.apart, k0, n);
-    float t[4] = {};
-    step_products<W, X>(t, w0[0], w1[0], first.x[0].used(x.v[g], k, n, !kTail));
-    if constexpr (!C::kBothSteps) first.x[0].load(x.v[g], x.apart, k + S, n);
-    step_products<W, X>(t, w0[1], w1[1], first.x[C::kBothSteps ? 1 : 0].used(x.v[g], k + S, n, !kTail));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (std::is_same<W, F8>::value) t[j] *= j < 2 ? f0 : f1;
-      c[g][j] += t[j];
-    }
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (std::is_same<W, F8>::value) t[j] *= j < 2 ? f0 : f1;
+    c[j] += t[j];
   }
 }
 
@@ -434,13 +443,13 @@ struct Matrix {
   uint64_t rows, stride;  // stride: bytes
   uint32_t bytes;         // of a row
 };
-template <uint32_t kStages, bool kShift, class Fill>
+template <bool kShift, class Fill>
 struct Stages {
   Ring& ring;
   uint8_t* memory;
   const Matrix& matrix;
   Fill& fill;
-  uint32_t warp, stage = 0, parity = 0, number = 0;
+  uint32_t count, warp, stage = 0, parity = 0, number = 0;  // count: of the stages
   bool ok = true;
   unsigned int* ran_out;
 
@@ -462,9 +471,9 @@ struct Stages {
       tma_load_2d(to + 8 * kPiece, matrix.map, (int32_t)(fill.piece * (kPiece / 8)), (int32_t)fill.row1, &ring.full[st]);
     }
   }
-  __device__ __forceinline__ Stages(Ring& r, uint8_t* m, const Matrix& x, Fill& f, unsigned int* flag)
-      : ring(r), memory(m), matrix(x), fill(f), warp(threadIdx.x / 32), ran_out(flag) {
-    for (uint32_t i = 0; i < kStages; ++i) {
+  __device__ __forceinline__ Stages(Ring& r, uint8_t* m, const Matrix& x, Fill& f, uint32_t n, unsigned int* flag)
+      : ring(r), memory(m), matrix(x), fill(f), count(n), warp(threadIdx.x / 32), ran_out(flag) {
+    for (uint32_t i = 0; i < count; ++i) {
       if (!fill.more()) break;
       if (warp == 0) ask(i);
       fill.advance();
@@ -491,29 +500,39 @@ struct Stages {
     next();
   }
   __device__ __forceinline__ void next() {
-    if (++stage == kStages) stage = 0, parity ^= 1;
+    if (++stage == count) stage = 0, parity ^= 1;
   }
   // A block that gives up does not end under its own copies.
   __device__ __forceinline__ void end() {
     if (ok) return;
     atomicOr(ran_out, 1u);
-    for (uint32_t i = 0; i < kStages; ++i, next()) wait_phase(&ring.full[stage], parity);
+    for (uint32_t i = 0; i < count; ++i, next()) wait_phase(&ring.full[stage], parity);
   }
 };
 // Barriers of the working warps: all wait, or a warp arrives and goes on.
 __device__ __forceinline__ void warps_sync(uint32_t id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void warps_arrive(uint32_t id) { asm volatile("bar.arrive %0, 256;" ::"r"(id) : "memory"); }
 
-// ---- what both kernels know of the pairs: the active experts in order, where each
-// one's pairs begin, each pair's token and weight
-template <int G>
+// ---- what both kernels know of the pairs: the active experts in order, one with
+// more than 8 tokens several times, where the pairs of each entry begin (8 at most),
+// each pair's token and weight.  An entry beyond the first reads its matrices again,
+// from the L2 cache as a rule: neighbouring blocks take it at the same time.  (All
+// of an expert's tokens in one entry, four times 8 sums: the registers did not hold
+// what 8-bit weights become, 515 us where 16-bit ones took 258; 32 tokens, 8 of 128
+// experts.)
 struct Pairs {
-  static constexpr uint32_t N = 8 * G * kMaxTopK;
-  uint32_t count;  // active experts
-  float weight[N];  // of each pair (first kernel)
-  uint16_t expert[N];
-  uint16_t begin[N + 1];
-  uint8_t token[N];
+  uint32_t* count;
+  float* weight;  // of each pair (first kernel)
+  uint16_t *expert, *begin;
+  uint8_t* token;
+  __host__ __device__ static constexpr size_t bytes(uint32_t pairs) { return (16 + 9ull * pairs + 2 + 15) / 16 * 16; }
+  __device__ __forceinline__ Pairs(uint8_t* memory, uint32_t pairs) {
+    count = reinterpret_cast<uint32_t*>(memory);
+    weight = reinterpret_cast<float*>(memory + 16);
+    begin = reinterpret_cast<uint16_t*>(weight + pairs);
+    expert = begin + pairs + 1;
+    token = reinterpret_cast<uint8_t*>(expert + pairs);
+  }
 };
 // Where the pairs come from: ids and weights [tokens][top_k], the tokens of each
 // expert and where its pairs begin.
@@ -526,8 +545,8 @@ struct PairSource {
 
 // Ids outside the experts take no part.  All threads call it, after a barrier that
 // covers ids and weights.  Afterwards the source's memory may be given to copies.
-template <bool kWeights, int G>
-__device__ __forceinline__ void gather_pairs(Pairs<G>& p, PairSource& s, uint32_t tokens, uint32_t top_k, uint32_t experts) {
+template <bool kWeights>
+__device__ __forceinline__ void gather_pairs(const Pairs& p, PairSource& s, uint32_t tokens, uint32_t top_k, uint32_t experts) {
   const uint32_t lane = threadIdx.x % 32, pairs = tokens * top_k;
   for (uint32_t e = threadIdx.x; e < experts; e += kThreads) s.mask[e] = 0;
   __syncthreads();
@@ -538,17 +557,17 @@ __device__ __forceinline__ void gather_pairs(Pairs<G>& p, PairSource& s, uint32_
     uint32_t active = 0, begin = 0;
     for (uint32_t e0 = 0; e0 < experts; e0 += 32) {
       const uint32_t e = e0 + lane, mask = e < experts ? s.mask[e] : 0, n = __popc(mask);
-      const uint32_t upto = begin + warp_inclusive_sum(n), who = __ballot_sync(kAll, n > 0);
+      const uint32_t entries = (n + kTokens - 1) / kTokens;
+      const uint32_t upto = begin + warp_inclusive_sum(n), last = active + warp_inclusive_sum(entries);
       if (e < experts) s.place[e] = (uint16_t)(upto - n);
-      if (n) {
-        const uint32_t a = active + __popc(who & ((1u << lane) - 1));
-        p.expert[a] = (uint16_t)e;
-        p.begin[a] = (uint16_t)(upto - n);
+      for (uint32_t i = 0; i < entries; ++i) {
+        p.expert[last - entries + i] = (uint16_t)e;
+        p.begin[last - entries + i] = (uint16_t)(upto - n + i * kTokens);
       }
-      active += __popc(who);
+      active = __shfl_sync(kAll, last, 31);
       begin = __shfl_sync(kAll, upto, 31);
     }
-    if (lane == 0) p.count = active, p.begin[active] = (uint16_t)begin;
+    if (lane == 0) *p.count = active, p.begin[active] = (uint16_t)begin;
   }
   __syncthreads();
   for (uint32_t i = threadIdx.x; i < pairs; i += kThreads) {
@@ -591,16 +610,18 @@ cudaError_t clusters_at_once(void (*kernel)(P...), std::atomic<int>* known, size
 // 175 us with an early start, 142 without).
 template <class... P, class... A>
 cudaError_t launch_clusters(void (*kernel)(P...), uint32_t clusters, size_t smem, cudaStream_t s, const A&... args) {
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = kCluster, at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = kCluster, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = clusters * kCluster, cfg.blockDim = kThreads, cfg.dynamicSmemBytes = smem, cfg.stream = s;
-  cfg.attrs = &at, cfg.numAttrs = 1;
+  cfg.attrs = at, cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// The kernels, by their tokens: up to 8, or any number (zc_layer_up.cu, zc_layer_down.cu).
+// zc_layer_up.cu, zc_layer_down.cu
 cudaError_t layer_up_launch(const LayerArgs& a, int type, bool blocks, cudaStream_t s);
 cudaError_t layer_down_launch(const LayerArgs& a, int type, bool blocks, cudaStream_t s);
 cudaError_t layer_up_waits(cudaStream_t s, bool* ran_out);

@@ -7,27 +7,34 @@ namespace {
 
 __device__ unsigned int g_layer_down_ran_out;
 
+// Dynamic shared memory: the stages (before them the pairs' source), the warps'
+// sums and a round's; behind them the pairs.
+template <bool kShift>
+__host__ __device__ __forceinline__ size_t down_memory(uint32_t tokens, uint32_t stages) {
+  return stages * kStageBytes<kShift> + 4ull * (kWarps + kCluster) * tokens * 16;
+}
+
 // 16 hidden places at a time; the pieces of the active experts' rows, one expert
 // after the other, are dealt out in equal runs to 1, 2, 4 or 8 blocks of a cluster:
 // whichever leaves the fewest pieces to the block that has most.  A warp adds what an
 // expert gives to its tokens' sums in shared memory: an expert's columns are its own
 // tokens only, so that nothing of it reaches another's.  A block adds its warps', and after 8 tiles the
 // blocks that share them each all blocks' of some of them.
-template <bool kShift, class T, class W, int G>
-__device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs<G>& pairs, Ring& ring, uint8_t* memory) {
-  constexpr uint32_t kStages = kStagesOf<G>, kRound = kCluster;  // tiles before the blocks' sums are added
-  using X = PartsFor<W>;
+template <bool kShift, class T, class W>
+__device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs& pairs, Ring& ring, uint8_t* memory) {
+  constexpr uint32_t kRound = kCluster;  // tiles before the blocks' sums are added
+  using X = PartsFor<T>;
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, gid = lane / 4, quad = lane % 4;
   const uint32_t rank = cluster_rank(), cluster = blockIdx.x / kCluster, clusters = gridDim.x / kCluster;
   const uint32_t size = a.tokens * 16;  // of a tile: [token][place]
-  float* warps = reinterpret_cast<float*>(memory + kStages * kStageBytes<kShift>);
+  float* warps = reinterpret_cast<float*>(memory + a.stages * kStageBytes<kShift>);
   float* own = warps + warp * size;        // a warp's sums
   float* block = warps + kWarps * size;    // a block's, of a round's tiles
   const auto* h = static_cast<const typename X::Value*>(a.h);
   const uint64_t apart = (uint64_t)a.tokens * a.top_k * a.h_stride;
   // whole chunks of a row, and their pieces (one at least); what is left is a warp's of the block that has a row's last
   const uint32_t body = a.inner / kPlacesOfChunk<W> * kPlacesOfChunk<W>, pieces = max((body + kPlacesOfPiece<W> - 1) / kPlacesOfPiece<W>, 1u);
-  const uint32_t all = pieces * pairs.count;
+  const uint32_t all = pieces * *pairs.count;
   const uint32_t tiles = (a.hidden + 15) / 16, across = (a.inner + kFp8Block - 1) / kFp8Block;
   uint32_t split = 1, fewest = 0xFFFFFFFFu;
   for (uint32_t s = 1; s <= kCluster; s *= 2) {
@@ -40,7 +47,7 @@ __device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs<G>& p
   const uint32_t from = (uint32_t)((uint64_t)all * part / split), upto = (uint32_t)((uint64_t)all * (part + 1) / split);
   struct Fill {
     const LayerArgs& a;
-    const Pairs<G>& pairs;
+    const Pairs& pairs;
     uint32_t tile, tiles, stride, s, from, upto, pieces;
     bool any;
     uint32_t piece = 0, row0 = 0, row1 = 0;
@@ -59,7 +66,7 @@ __device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs<G>& p
   } fill{a, pairs, t0, tiles, stride, from, from, upto, pieces, body > 0};
   fill.place();
   const Matrix matrix = {&a.down_map, static_cast<const uint8_t*>(a.down), (uint64_t)a.experts * a.hidden, a.down_stride * sizeof(W), a.inner * (uint32_t)sizeof(W)};
-  Stages<kStages, kShift, Fill> stages(ring, memory, matrix, fill, &g_layer_down_ran_out);
+  Stages<kShift, Fill> stages(ring, memory, matrix, fill, a.stages, &g_layer_down_ran_out);
   const uint32_t k0 = warp * kPlacesOfChunk<W>;
   const auto vector = [&](uint32_t n, uint32_t col) -> const typename X::Value* {  // of a column of active expert n
     uint32_t at = pairs.begin[n] + col;
@@ -74,16 +81,13 @@ __device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs<G>& p
       const uint32_t tile = t0 + (round * kRound + j) * stride;
       if (tile >= tiles) break;
       const uint32_t r0 = min(tile * 16 + gid, a.hidden - 1), r1 = min(tile * 16 + gid + 8, a.hidden - 1);
-      float c[G][4] = {};
+      float c[4] = {};
       for (uint32_t i = lane; i < size; i += 32) own[i] = 0.0f;
       __syncwarp();
       uint32_t n = from / pieces, p = from - n * pieces;
       for (uint32_t s = from; s < upto;) {  // an expert's pieces of the run
         const uint32_t begin = pairs.begin[n], tokens = pairs.begin[n + 1] - begin;
-        Vectors<X, G> v;
-        v.apart = apart, v.groups = (tokens + 7) / 8;
-#pragma unroll
-        for (int g = 0; g < G; ++g) v.v[g] = vector(n, g * 8 + gid);
+        const Vector<X> v = {vector(n, gid), apart};
         const W* at = static_cast<const W*>(a.down) + (uint64_t)pairs.expert[n] * a.hidden * a.down_stride;
         const uint8_t* scales = a.down_scales + (uint64_t)pairs.expert[n] * ((a.hidden + kFp8Block - 1) / kFp8Block) * across;
         const Rows<W> its = {at + r0 * a.down_stride, at + r1 * a.down_stride, scales + r0 / kFp8Block * across, scales + r1 / kFp8Block * across};
@@ -100,25 +104,21 @@ __device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs<G>& p
 #pragma unroll
           for (int i = 0; i < 2; ++i, k += kWarps * kPlacesOfChunk<W>) {
             const bool leaves = i && p + 1 == last;
-            x[i ^ 1].load(leaves ? after : v.v[0], apart, leaves ? after_k : k + kWarps * kPlacesOfChunk<W>, a.inner);
-            if (k < body) take_chunk<false, kShift, false, W, X, G>(c, stage + i * kWarps * kChunk, its, v, x[i], k, a.inner);
+            x[i ^ 1].load(leaves ? after : v.at, apart, leaves ? after_k : k + kWarps * kPlacesOfChunk<W>, a.inner);
+            if (k < body) take_chunk<false, kShift, false, W, X>(c, stage + i * kWarps * kChunk, its, v, x[i], k, a.inner);
           }
           if (body) stages.leave();
         }
         if (to_end && body < a.inner && warp == n % kWarps) {
-          x[1].load(v.v[0], apart, body, a.inner);
-          take_chunk<true, kShift, false, W, X, G>(c, nullptr, its, v, x[1], body, a.inner);
+          x[1].load(v.at, apart, body, a.inner);
+          take_chunk<true, kShift, false, W, X>(c, nullptr, its, v, x[1], body, a.inner);
         }
         p = 0, ++n;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          if (g >= (int)v.groups) break;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t col = g * 8 + quad * 2 + i % 2;
-            if (col < tokens) own[pairs.token[begin + col] * 16 + gid + (i / 2) * 8] += c[g][i];
-            c[g][i] = 0.0f;
-          }
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t col = quad * 2 + i % 2;
+          if (col < tokens) own[pairs.token[begin + col] * 16 + gid + (i / 2) * 8] += c[i];
+          c[i] = 0.0f;
         }
         __syncwarp();
       }
@@ -138,7 +138,7 @@ __device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs<G>& p
         const uint32_t t = i / 16, place = tile * 16 + i % 16;
         if (place >= a.hidden) continue;
         float sum = a.residual ? to_float(static_cast<const T*>(a.residual)[(uint64_t)t * a.hidden + place]) : 0.0f;
-        for (uint32_t r = first; r < first + split; ++r) sum += load_cluster(at_rank(block + j * size + i, r));
+        sum += cluster_sum(block + j * size + i, first, split);
         static_cast<T*>(a.y)[(uint64_t)t * a.hidden + place] = from_float<T>(sum);
       }
     }
@@ -147,17 +147,19 @@ __device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs<G>& p
   stages.end();
 }
 
-template <bool kShift, class T, class W, int G>
+template <bool kShift, class T, class W>
 __global__ void __launch_bounds__(kThreads, 2) zc_layer_down_kernel(const __grid_constant__ LayerArgs a) {
   extern __shared__ __align__(1024) uint8_t s_dyn[];
-  __shared__ Pairs<G> s_pairs;
   __shared__ Ring s_ring;
   PairSource& source = *reinterpret_cast<PairSource*>(s_dyn);
   ring_init(s_ring);
+  pdl_wait();
   for (uint32_t i = threadIdx.x; i < a.tokens * a.top_k; i += kThreads) source.ids[i] = (uint32_t)a.ids[i];
   __syncthreads();
-  gather_pairs<false>(s_pairs, source, a.tokens, a.top_k, a.experts);
-  layer_down<kShift, T, W, G>(a, s_pairs, s_ring, s_dyn);
+  const Pairs pairs(s_dyn + down_memory<kShift>(a.tokens, a.stages), a.tokens * a.top_k);
+  gather_pairs<false>(pairs, source, a.tokens, a.top_k, a.experts);
+  layer_down<kShift, T, W>(a, pairs, s_ring, s_dyn);
+  pdl_trigger();
 }
 
 // experts that a lane of choose_any holds
@@ -166,31 +168,22 @@ uint32_t held_by_lane(uint32_t experts) {
 }
 
 
-template <int G>
-size_t down_smem(uint32_t tokens, bool shift) {
-  return kStagesOf<G> * (shift ? kStageBytes<true> : kStageBytes<false>) + 4ull * (kWarps + kCluster) * tokens * 16;
-}
-
-template <bool kShift, class T, class W, int G>
-cudaError_t down_launch(const LayerArgs& a, cudaStream_t s) {
-  static std::atomic<int> known[kMaxDevices];
-  constexpr uint32_t most = G == 1 ? 8 : kMaxTokens;
-  const auto kernel = zc_layer_down_kernel<kShift, T, W, G>;
-  int clusters = 0;
-  const cudaError_t e = clusters_at_once(kernel, known, down_smem<G>(most, kShift), down_smem<G>(most, kShift), &clusters);
-  const uint32_t tiles = (a.hidden + 15) / 16;
-  return e != cudaSuccess ? e : launch_clusters(kernel, std::min<uint32_t>(clusters, tiles), down_smem<G>(a.tokens, kShift), s, a);
-}
-
 template <bool kShift, class T, class W>
-cudaError_t down_by_tokens(const LayerArgs& a, cudaStream_t s) {
-  return a.tokens <= 8 ? down_launch<kShift, T, W, 1>(a, s) : down_launch<kShift, T, W, 4>(a, s);
+cudaError_t down_launch(LayerArgs a, cudaStream_t s) {
+  static std::atomic<int> known[kMaxDevices];
+  const auto kernel = zc_layer_down_kernel<kShift, T, W>;
+  const uint32_t pairs = a.tokens * a.top_k, tiles = (a.hidden + 15) / 16;
+  a.stages = kMaxStages;
+  while (a.stages > 2 && down_memory<kShift>(a.tokens, a.stages) + Pairs::bytes(pairs) > kRoomForTwo) --a.stages;
+  int clusters = 0;
+  const cudaError_t e = clusters_at_once(kernel, known, kRoomForTwo, down_memory<kShift>(kMaxTokens, kMaxStages) + Pairs::bytes(kMaxTokens * kMaxTopK), &clusters);
+  return e != cudaSuccess ? e : launch_clusters(kernel, std::min<uint32_t>(clusters, tiles), down_memory<kShift>(a.tokens, a.stages) + Pairs::bytes(pairs), s, a);
 }
 
 template <class T>
 cudaError_t down_by_weights(const LayerArgs& a, bool blocks, cudaStream_t s) {
-  if (blocks) return down_by_tokens<false, T, F8>(a, s);  // rows of codes start at multiples of 16
-  return a.shift_down ? down_by_tokens<true, T, T>(a, s) : down_by_tokens<false, T, T>(a, s);
+  if (blocks) return down_launch<false, T, F8>(a, s);  // rows of codes start at multiples of 16
+  return a.shift_down ? down_launch<true, T, T>(a, s) : down_launch<false, T, T>(a, s);
 }
 
 }  // namespace
@@ -210,7 +203,7 @@ extern "C" {
 
 zipccl_status zipccl_moe_layer_workspace_bytes(uint64_t tokens, uint32_t top_k, uint64_t inner, uint64_t* out_bytes) {
   if (!out_bytes || tokens > kMaxTokens || top_k == 0 || top_k > kMaxTopK || inner >= (1ull << 22)) return ZIPCCL_ERR_INVALID_ARG;
-  *out_bytes = (tokens * top_k * ((inner + 7) / 8 * 8) * 8 + 255) / 256 * 256;  // two floats or three bfloat16 a value
+  *out_bytes = (tokens * top_k * ((inner + 7) / 8 * 8) * 8 + 255) / 256 * 256;  // two floats a value
   return ZIPCCL_OK;
 }
 
