@@ -102,14 +102,8 @@ __device__ __forceinline__ float cluster_sum(const float* p, uint32_t first, uin
 struct F8 {
   uint8_t bits;
 };
-template <class W>
-constexpr int kPer16 = 16 / sizeof(W);
 
-// 16 bytes of a row that starts anywhere: the two multiples of 16 that they lie in.
-struct Raw {
-  uint4 a, b;
-};
-// ... from byte `off` on (a multiple of 16 from the row's start) of `bytes`.  What
+// 16 bytes of a row that starts anywhere, from byte `off` on (a multiple of 16 from the row's start) of `bytes`.  What
 // lies behind the row is read from its last 16 bytes: no access leaves the 16 that
 // hold one of its values.
 template <bool kShift>
@@ -125,21 +119,6 @@ __device__ __forceinline__ Raw raw16(const void* row, uint32_t off, uint32_t byt
   }
   return r;
 }
-// The 16 bytes from byte `shift` on.
-template <bool kShift>
-__device__ __forceinline__ uint4 settle(const Raw& r, uint32_t shift) {
-  if constexpr (!kShift) return r.a;
-  uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-#pragma unroll
-  for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
-  const uint32_t bits = shift % 4 * 8;
-  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
-                    __funnelshift_r(w[3], w[4], bits));
-}
-__device__ __forceinline__ uint32_t shift_of(const void* p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15); }
-
 // Values 2 j and 2 j + 1 of 16 bytes, exact.
 template <class W>
 __device__ __forceinline__ float2 two_of(const uint4& q, int j) {
@@ -201,20 +180,6 @@ template <class W>
 constexpr uint32_t kPlacesOfChunk = kChunk / sizeof(W);
 template <class W>
 constexpr uint32_t kPlacesOfPiece = kPiece / sizeof(W);
-
-// Zeros behind the first `left` of 16 bytes of values.
-template <class W>
-__device__ __forceinline__ uint4 keep(uint4 q, int left) {
-  if (left >= kPer16<W>) return q;
-  uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int bytes = left * (int)sizeof(W) - 4 * i;
-    if (bytes <= 0) w[i] = 0;
-    else if (bytes < 4) w[i] &= (1u << (8 * bytes)) - 1;
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // h as the second kernel takes it, each part in an array of its own.  Where the
 // layer's type has 16 bits two bfloat16 values: 16 bits, 2^-17 of h off at most,

@@ -65,6 +65,43 @@ __device__ __forceinline__ Pack<__half, 8> rounded<__half, 8>(const float (&x)[8
   return p;
 }
 
+// ---- rows that start anywhere, in aligned accesses
+template <class W>
+constexpr int kPer16 = 16 / sizeof(W);  // values in 16 bytes
+
+// 16 bytes of a row that starts anywhere: the two multiples of 16 that they lie in.
+struct Raw {
+  uint4 a, b;
+};
+// The 16 bytes from byte `shift` on.
+template <bool kShift>
+__device__ __forceinline__ uint4 settle(const Raw& r, uint32_t shift) {
+  if constexpr (!kShift) return r.a;
+  uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+  const uint32_t bits = shift % 4 * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                    __funnelshift_r(w[3], w[4], bits));
+}
+__device__ __forceinline__ uint32_t shift_of(const void* p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15); }
+
+// Zeros behind the first `left` of 16 bytes of values.
+template <class W>
+__device__ __forceinline__ uint4 keep(uint4 q, int left) {
+  if (left >= kPer16<W>) return q;
+  uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int bytes = left * (int)sizeof(W) - 4 * i;
+    if (bytes <= 0) w[i] = 0;
+    else if (bytes < 4) w[i] &= (1u << (8 * bytes)) - 1;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A kernel that is launched by launch() begins with after_previous(): it may be
 // set up while the kernel before it in the stream still runs.  Its blocks start
 // as that one's last blocks leave room and wait here, before they touch memory,

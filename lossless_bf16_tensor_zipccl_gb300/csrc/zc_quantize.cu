@@ -10,7 +10,6 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "zc_fp8.cuh"
 #include "zipccl.h"
@@ -38,19 +37,36 @@ struct Sixteen {
       w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
     }
   }
-  __device__ __forceinline__ void set(int i, T x) {  // i is known at compile time
-    if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(to_float(x));
-    else w[i / 2] = i % 2 ? (w[i / 2] & 0xFFFFu) | (uint32_t)bits(x) << 16 : (w[i / 2] & 0xFFFF0000u) | bits(x);
+  // Places col .. of a row of `cols` that starts anywhere (kShift) or at a multiple of
+  // 16 bytes; zeros behind it.  No access leaves the 16 bytes that hold one of its values.
+  template <bool kShift>
+  __device__ __forceinline__ void load(const T* row, uint32_t col, uint32_t cols) {
+    if constexpr (kShift) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(row), base = at & ~uintptr_t(15);
+      const uint32_t shift = (uint32_t)(at & 15);
+      const uint64_t off = (uint64_t)col * sizeof(T), last = (shift + (uint64_t)cols * sizeof(T) - 1) & ~uint64_t(15);
+      uint4 v[kWords / 4 + 1];
+#pragma unroll
+      for (int i = 0; i <= kWords / 4; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(base + min(off + 16 * i, last)));
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) put(i, settle<true>({v[i], v[i + 1]}, shift));
+    } else if (col + 16 <= cols) {
+      load(row + col);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i)
+        put(i, __ldg(reinterpret_cast<const uint4*>(row + min(col + i * kPer16<T>, (cols - 1) / kPer16<T> * kPer16<T>))));
+    }
+    if (col + 16 > cols) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) put(i / 4, keep<T>(make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]), (int)cols - (int)col - i / 4 * kPer16<T>));
+    }
   }
+  __device__ __forceinline__ void put(int i, const uint4& v) { w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w; }
   __device__ __forceinline__ float get(int i) const {
     if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
     else if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
     else return __half2float(__ushort_as_half((unsigned short)(i % 2 ? w[i / 2] >> 16 : w[i / 2])));
-  }
-  static __device__ __forceinline__ uint32_t bits(T x) {
-    uint32_t b = 0;
-    memcpy(&b, &x, sizeof(T));
-    return b;
   }
 };
 
@@ -61,8 +77,11 @@ struct Magnitude {
   static constexpr bool kPair = sizeof(T) == 2;
   static __device__ __forceinline__ uint32_t of(uint32_t w) { return w & (kPair ? 0x7FFF7FFFu : 0x7FFFFFFFu); }
   static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
-    if constexpr (kPair) return __vmaxu2(a, b);
-    else return a > b ? a : b;
+    return max(a, b, b);
+  }
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b, uint32_t c) {  // one instruction
+    if constexpr (kPair) return __vimax3_u16x2(a, b, c);
+    else return __vimax3_u32(a, b, c);
   }
   // the same without what is not finite
   static __device__ __forceinline__ uint32_t finite(uint32_t w) {
@@ -90,7 +109,10 @@ __device__ __forceinline__ uint32_t top_of(const Sixteen<T>& x) {
   using M = Magnitude<T>;
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < Sixteen<T>::kWords; ++i) m = M::max(m, kFinite ? M::finite(x.w[i]) : M::of(x.w[i]));
+  for (int i = 0; i < Sixteen<T>::kWords; i += 2) {
+    if constexpr (kFinite) m = M::max(m, M::finite(x.w[i]), M::finite(x.w[i + 1]));
+    else m = M::max(m, M::of(x.w[i]), M::of(x.w[i + 1]));
+  }
   return M::as_float(M::fold(m));
 }
 
@@ -136,9 +158,9 @@ struct RowArgs {
   uint32_t cols, blocks;                 // blocks of a row
 };
 
-// Along the rows.  Aligned rows: 8 lanes take a block, 16 values each, in
-// 16-byte loads and one 16-byte store.
-template <class T>
+// Along the rows: 8 lanes take a block, 16 values each, in 16-byte loads and one
+// 16-byte store.
+template <class T, bool kShift>
 __global__ void __launch_bounds__(kThreads) zc_quantize_rows_kernel(RowArgs a) {
   after_previous();
   const uint32_t part = threadIdx.x % 8;
@@ -150,16 +172,9 @@ __global__ void __launch_bounds__(kThreads) zc_quantize_rows_kernel(RowArgs a) {
     const uint64_t row = in ? (a.groups >> 32 ? g / a.blocks : (uint32_t)g / a.blocks) : 0;
     const uint32_t block = in ? (uint32_t)(g - row * a.blocks) : 0;
     const uint32_t col = block * kFp8Block + part * 16;
-    const T* p = static_cast<const T*>(a.x) + row * a.stride + col;
     Sixteen<T> x;
     x.clear();
-    if (in && col + 16 <= a.cols) {
-      x.load(p);
-    } else if (in) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (col + i < a.cols) x.set(i, p[i]);
-    }
+    if (in && col < a.cols) x.template load<kShift>(static_cast<const T*>(a.x) + row * a.stride, col, a.cols);
     uint32_t m = top_of<T, false>(x);
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
@@ -180,51 +195,6 @@ __global__ void __launch_bounds__(kThreads) zc_quantize_rows_kernel(RowArgs a) {
   }
 }
 
-// Rows that start anywhere: a warp takes kFew blocks at a time, lane by lane, so
-// that each access of the warp is one run of 32 values.
-constexpr int kFew = 4;
-template <class T>
-__global__ void __launch_bounds__(kThreads) zc_quantize_odd_rows_kernel(RowArgs a) {
-  after_previous();
-  const uint32_t lane = threadIdx.x % 32;
-  const uint64_t per_grid = (uint64_t)gridDim.x * (kThreads / 32) * kFew;
-  for (uint64_t g0 = ((uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kFew; g0 < a.groups; g0 += per_grid) {
-    float v[kFew][4];
-#pragma unroll
-    for (int b = 0; b < kFew; ++b) {
-      const uint64_t g = min(g0 + b, a.groups - 1);
-      const uint64_t row = g / a.blocks;
-      const uint32_t col = (uint32_t)(g - row * a.blocks) * kFp8Block + lane;
-      const T* p = static_cast<const T*>(a.x) + row * a.stride + col;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[b][i] = col + 32 * i < a.cols ? to_float(__ldcs(p + 32 * i)) : 0.0f;
-    }
-#pragma unroll
-    for (int b = 0; b < kFew; ++b) {
-      const uint64_t g = g0 + b;
-      if (g >= a.groups) break;
-      uint32_t m = 0;
-      bool odd[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w = __float_as_uint(v[b][i]) & 0x7FFFFFFFu;
-        odd[i] = w >= kInf;
-        m = max(m, odd[i] ? 0 : w);
-      }
-      const uint32_t s = scale_byte(__reduce_max_sync(kAll, m));
-      const float by = scale_inverse(s);
-      const uint64_t row = g / a.blocks;
-      const uint32_t col = (uint32_t)(g - row * a.blocks) * kFp8Block + lane;
-      uint8_t* c = a.codes + row * a.code_stride + col;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (col + 32 * i < a.cols)
-          c[32 * i] = (uint8_t)__nv_cvt_float_to_fp8(odd[i] ? __uint_as_float(0x7FC00000u) : v[b][i] * by, __NV_SATFINITE, __NV_E4M3);
-      if (lane == 0) a.scales[g] = (uint8_t)s;
-    }
-  }
-}
-
 // Down the columns, and 128 x 128 blocks: a block of the grid takes tiles of
 // 128 rows x 128 columns.  A thread holds 16 columns of 4 rows (32 apart).
 enum Form { kColumns, kBoth, kWeights };
@@ -237,17 +207,15 @@ struct TileArgs {
   uint32_t rows, cols, chunks;  // weights: rows of a matrix, and the matrices
   uint32_t scale_rows;          // columns: rows of the scales
   uint32_t tiles, turn;         // tiles along a row; how many of them a block of the grid takes
-  bool wide;
 };
 
 constexpr int kTileRows = 128;
 
-template <class T, int kForm>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) zc_quantize_tiles_kernel(TileArgs a) {
+template <class T, int kForm, bool kShift>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? (kShift || kForm == kBoth ? 3 : 4) : 2) zc_quantize_tiles_kernel(TileArgs a) {
   using M = Magnitude<T>;
   constexpr int W = Sixteen<T>::kWords;
   after_previous();
-  extern __shared__ __align__(16) uint8_t s_raw[];  // rows that start anywhere: the tile
   __shared__ __align__(16) uint32_t s_top[8][4 * W * 2];
   __shared__ __align__(16) float s_by[kTileRows];
   const uint32_t part = threadIdx.x % 8, line = threadIdx.x / 8, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -291,38 +259,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) zc_quantize_
     Sixteen<T> x[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j].clear();
-    if (a.wide) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const T* p = base + (uint64_t)(line + 32 * j) * a.stride + col;
-        if (line + 32 * j >= span.count) continue;
-        if (col + 16 <= a.cols) {
-          x[j].load(p);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (col + i < a.cols) x[j].set(i, p[i]);
-        }
-      }
-    } else {  // through shared memory: a warp reads runs of 32 values
-      T* s = reinterpret_cast<T*>(s_raw);
-      __syncthreads();
-#pragma unroll 4
-      for (uint32_t i = threadIdx.x; i < kTileRows * kFp8Block; i += kThreads) {
-        const uint32_t r = i / kFp8Block, c = i % kFp8Block;
-        if (r < span.count) s[i] = col0 + c < a.cols ? __ldcs(base + (uint64_t)r * a.stride + col0 + c) : from_float<T>(0.0f);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (line + 32 * j < span.count) {
-#pragma unroll
-          for (int i = 0; i < W; i += 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(s_raw + ((line + 32 * j) * kFp8Block + part * 16) * sizeof(T) + 4 * i);
-            x[j].w[i] = v.x, x[j].w[i + 1] = v.y, x[j].w[i + 2] = v.z, x[j].w[i + 3] = v.w;
-          }
-        }
-    }
+    for (int j = 0; j < 4; ++j)
+      if (line + 32 * j < span.count && col < a.cols) x[j].template load<kShift>(base + (uint64_t)(line + 32 * j) * a.stride, col, a.cols);
     uint32_t all = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) all = max(all, top_of<T, false>(x[j]));
@@ -371,9 +310,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) zc_quantize_
       uint32_t m[W];
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        m[i] = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m[i] = M::max(m[i], odd ? M::finite(x[j].w[i]) : M::of(x[j].w[i]));
+        if (odd) m[i] = M::max(M::max(M::finite(x[0].w[i]), M::finite(x[1].w[i])), M::finite(x[2].w[i]), M::finite(x[3].w[i]));
+        else m[i] = M::max(M::max(M::of(x[0].w[i]), M::of(x[1].w[i])), M::of(x[2].w[i]), M::of(x[3].w[i]));
         m[i] = M::max(m[i], __shfl_xor_sync(kAll, m[i], 8));
         m[i] = M::max(m[i], __shfl_xor_sync(kAll, m[i], 16));
       }
@@ -419,50 +357,35 @@ bool good_codes(const void* codes, uint64_t stride, uint64_t cols) {
 }
 
 template <class T>
-cudaError_t rows_by_type(const RowArgs& a, bool wide, cudaStream_t s) {
-  const uint64_t per = wide ? kThreads / 8 : kThreads / 32 * kFew;
-  const uint32_t grid = (uint32_t)std::min<uint64_t>((a.groups + per - 1) / per, 152 * 32);
-  return launch(wide ? zc_quantize_rows_kernel<T> : zc_quantize_odd_rows_kernel<T>, grid, kThreads, 0, s, a);
+cudaError_t rows_by_type(const RowArgs& a, bool shift, cudaStream_t s) {
+  const uint32_t grid = (uint32_t)std::min<uint64_t>((a.groups + kThreads / 8 - 1) / (kThreads / 8), 152 * 32);
+  return launch(shift ? zc_quantize_rows_kernel<T, true> : zc_quantize_rows_kernel<T, false>, grid, kThreads, 0, s, a);
 }
 
-// Shared memory for a tile of rows that start anywhere: 64 KB for floats, allowed
-// once for each device (the limit is the kernel's own and never lowered).
 template <class T, int kForm>
-cudaError_t tiles_launch(const TileArgs& a, uint64_t high, cudaStream_t s) {
-  const size_t smem = a.wide ? 0 : kTileRows * kFp8Block * sizeof(T);
-  if (smem > 40000) {
-    static std::atomic<bool> allowed[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (!allowed[dev].load(std::memory_order_acquire)) {
-      e = cudaFuncSetAttribute(zc_quantize_tiles_kernel<T, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-      allowed[dev].store(true, std::memory_order_release);
-    }
-  }
+cudaError_t tiles_launch(const TileArgs& a, uint64_t high, bool shift, cudaStream_t s) {
   const dim3 grid((uint32_t)high, (a.tiles + a.turn - 1) / a.turn);
-  return launch(zc_quantize_tiles_kernel<T, kForm>, grid, kThreads, smem, s, a);
+  return launch(shift ? zc_quantize_tiles_kernel<T, kForm, true> : zc_quantize_tiles_kernel<T, kForm, false>, grid, kThreads, 0, s, a);
 }
 
 template <class T>
-cudaError_t tiles_by_form(const TileArgs& a, int form, uint64_t high, cudaStream_t s) {
-  return form == kWeights ? tiles_launch<T, kWeights>(a, high, s)
-         : form == kBoth  ? tiles_launch<T, kBoth>(a, high, s)
-                          : tiles_launch<T, kColumns>(a, high, s);
+cudaError_t tiles_by_form(const TileArgs& a, int form, uint64_t high, bool shift, cudaStream_t s) {
+  return form == kWeights ? tiles_launch<T, kWeights>(a, high, shift, s)
+         : form == kBoth  ? tiles_launch<T, kBoth>(a, high, shift, s)
+                          : tiles_launch<T, kColumns>(a, high, shift, s);
 }
 
 cudaError_t tiles_by_type(TileArgs& a, int type, int form, uint64_t high, cudaStream_t s) {
   const uint64_t z = type_bytes(type);
-  a.wide = host_aligned(a.x, 16) && a.stride * z % 16 == 0;
+  const bool shift = !host_aligned(a.x, 16) || a.stride * z % 16 != 0;
   a.tiles = (a.cols + kFp8Block - 1) / kFp8Block;
-  // a block of the grid takes several tiles of its rows where enough blocks are
-  // left: finding the rows among the chunks is paid once
-  a.turn = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(high * a.tiles / (152 * 6), 1), 8);
-  return type == ZIPCCL_TYPE_F32    ? tiles_by_form<float>(a, form, high, s)
-         : type == ZIPCCL_TYPE_BF16 ? tiles_by_form<__nv_bfloat16>(a, form, high, s)
-                                    : tiles_by_form<__half>(a, form, high, s);
+  // a block of the grid takes two tiles of its rows where enough blocks are left:
+  // finding the rows among the chunks is paid once (32,768 x 4,096 both ways: 135 us
+  // with one, 133 with two, 137 with eight)
+  a.turn = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(high * a.tiles / (152 * 6), 1), 2);
+  return type == ZIPCCL_TYPE_F32    ? tiles_by_form<float>(a, form, high, shift, s)
+         : type == ZIPCCL_TYPE_BF16 ? tiles_by_form<__nv_bfloat16>(a, form, high, shift, s)
+                                    : tiles_by_form<__half>(a, form, high, shift, s);
 }
 
 }  // namespace
@@ -487,11 +410,11 @@ zipccl_status zipccl_moe_quantize(const void* d_x, int type, uint64_t row_stride
   a.cols = (uint32_t)cols;
   a.blocks = (uint32_t)((cols + kFp8Block - 1) / kFp8Block);
   a.groups = rows * a.blocks;
-  const bool wide = host_aligned(d_x, 16) && row_stride * z % 16 == 0;
+  const bool shift = !host_aligned(d_x, 16) || row_stride * z % 16 != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = type == ZIPCCL_TYPE_F32    ? rows_by_type<float>(a, wide, s)
-                        : type == ZIPCCL_TYPE_BF16 ? rows_by_type<__nv_bfloat16>(a, wide, s)
-                                                   : rows_by_type<__half>(a, wide, s);
+  const cudaError_t e = type == ZIPCCL_TYPE_F32    ? rows_by_type<float>(a, shift, s)
+                        : type == ZIPCCL_TYPE_BF16 ? rows_by_type<__nv_bfloat16>(a, shift, s)
+                                                   : rows_by_type<__half>(a, shift, s);
   return e == cudaSuccess ? ZIPCCL_OK : ZIPCCL_ERR_CUDA;
 }
 
