@@ -6,11 +6,11 @@ A step of a rank:
   route -> plan -> dispatch -> [all-to-all] -> experts -> [all-to-all] -> combine
 and backwards, then for the ranks together
   gradients -> [reduce-scatter] -> AdamW -> [all-gather] -> parameters
-Every [exchange] is a compressed one.  Attention and the layer's gate and
-experts' products are left to torch: the example shows what the package does
-around them.
+Every [exchange] is a compressed one.  Attention and the layer's gate are left to
+torch, and so are the experts' products, or they run in 8-bit floating point
+(--fp8): then no chunk size is needed on the host for them.
 
-    python examples/moe_training_step.py --steps 20
+    python examples/moe_training_step.py --steps 20 [--fp8]
 """
 from __future__ import annotations
 
@@ -41,7 +41,8 @@ class Layer:
     """Gate and experts: float32 parameters with bfloat16 copies, one flat
     buffer, and AdamW states in 8 (or 32) bits."""
 
-    def __init__(self, hidden, experts, bits, seed=0):
+    def __init__(self, hidden, experts, bits, seed=0, fp8=False):
+        self.fp8 = fp8
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.hidden, self.experts, self.bits, self.steps = hidden, experts, bits, 0
         shapes = [(experts, hidden), (experts, hidden, hidden)]
@@ -66,8 +67,13 @@ class Layer:
         arrived = exchange(rows[:used], chunks)          # all-to-all: tokens to their experts
         out = torch.zeros_like(rows)
         pieces = arrived.split(counts)
-        for e, (a, o) in enumerate(zip(pieces, out[:used].split(counts))):
-            torch.matmul(a, self.up[e], out=o)
+        if self.fp8:
+            in_rows, in_columns = zc.moe_quantize_columns(arrived, plan.offsets, by_rows=True)
+            matrices = zc.moe_quantize_weights(self.up.mT.contiguous())
+            zc.moe_matmul(in_rows, matrices, plan.offsets, out=out[:used])
+        else:
+            for e, (a, o) in enumerate(zip(pieces, out[:used].split(counts))):
+                torch.matmul(a, self.up[e], out=o)
         out[:used] = exchange(out[:used], chunks)        # all-to-all: and back
         y = zc.moe_combine(out, plan.slots, weights, residual=x)
 
@@ -75,7 +81,11 @@ class Layer:
         grad_y = ((y.float() - target) * (2.0 / y.numel())).bfloat16()
         grad_out, grad_weights = zc.moe_combine_backward(grad_y, out, plan.slots, weights)
         grad_out = exchange(grad_out[:used], chunks)
-        grad_up = torch.stack([a.T @ g for a, g in zip(pieces, grad_out.split(counts))])
+        if self.fp8:
+            grad_columns = zc.moe_quantize_columns(grad_out, plan.offsets)
+            grad_up = zc.moe_matmul_backward_weights(grad_columns, in_columns, plan.offsets).mT
+        else:
+            grad_up = torch.stack([a.T @ g for a, g in zip(pieces, grad_out.split(counts))])
         grad_logits = zc.moe_route_backward(grad_weights, logits, ids)
         grad_gate = grad_logits.T @ x
         return loss, torch.cat([grad_gate.reshape(-1), grad_up.reshape(-1)]).bfloat16()
@@ -95,10 +105,10 @@ class Layer:
         self.copy.copy_(exchange(self.copy, [self.copy.numel()]))                     # all-gather of the parameters
 
 
-def train(steps=20, ranks=4, tokens=2048, hidden=512, experts=16, top_k=2, bits=8, lr=2e-3, seed=1):
+def train(steps=20, ranks=4, tokens=2048, hidden=512, experts=16, top_k=2, bits=8, lr=2e-3, seed=1, fp8=False):
     """Losses of `steps` steps on a fixed synthetic task, and the exchanges' compression ratio."""
     g = torch.Generator(device="cuda").manual_seed(seed)
-    layer = Layer(hidden, experts, bits)
+    layer = Layer(hidden, experts, bits, fp8=fp8)
     mix = torch.randn(hidden, hidden, generator=g, device="cuda") * hidden ** -0.5
     batches = [torch.randn(tokens, hidden, generator=g, device="cuda") for _ in range(ranks)]
     targets = [x + (x @ mix).relu() for x in batches]
@@ -117,6 +127,7 @@ def main():
                         ("bits", 8)):
         ap.add_argument("--" + name, type=int, default=value)
     ap.add_argument("--lr", type=float, default=2e-3)
+    ap.add_argument("--fp8", action="store_true", help="the experts' products in 8-bit floating point")
     losses, ratio = train(**{k.replace("-", "_"): v for k, v in vars(ap.parse_args()).items()})
     for i, loss in enumerate(losses):
         print(f"step {i:3d}  loss {loss:.5f}")

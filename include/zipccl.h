@@ -306,10 +306,10 @@ zipccl_status zipccl_codebook_rebuild_phase(int phase, int *base_offset, uint8_t
  * (parameters).  The conventions above hold, with these differences:
  *   - pointers need only the alignment of their element type; 16-byte
  *     aligned rows and tensors are the fast path;
- *   - the calls record no device status: every index read from device memory
- *     is checked against its range, and what is out of range takes no part,
- *     as each call says;
- *   - only zipccl_moe_plan needs a workspace;
+ *   - the calls record no device status (but for zipccl_moe_status): every
+ *     index read from device memory is checked against its range, and what is
+ *     out of range takes no part, as each call says;
+ *   - only zipccl_moe_plan and zipccl_moe_layer need a workspace;
  *   - results overlap neither inputs nor each other, but for what a call names.
  * Sums, softmax statistics, weights and states are computed in 32 bits; a
  * result of a 16-bit type is rounded once, to nearest even.  No call's
@@ -523,9 +523,9 @@ zipccl_status zipccl_moe_quantize_weights(const void *d_w, int type, uint32_t ex
  * weights of an empty chunk.  Sums are held in 32 bits on the tensor cores, in a
  * fixed order; out_type F32, BF16 or F16, rounded once.  out: rows out_stride
  * values apart, the WEIGHTS form's matrices `outer` rows apart.
- * A wait inside the kernel that runs out (2 s; not to be expected) leaves what
- * the block had not yet written unwritten and sets the device's word that
- * zipccl_moe_status reads and clears: ZIPCCL_OK or ZIPCCL_ERR_TIMEOUT
+ * A wait inside a kernel of this call or of zipccl_moe_layer that runs out (2 s;
+ * not to be expected) leaves its results undefined and sets a word of the current
+ * device that zipccl_moe_status reads and clears: ZIPCCL_OK or ZIPCCL_ERR_TIMEOUT
  * (synchronizes `stream`).
  */
 typedef enum { ZIPCCL_MATMUL_FORWARD = 0, ZIPCCL_MATMUL_BACKWARD = 1, ZIPCCL_MATMUL_WEIGHTS = 2 } zipccl_matmul_form;
@@ -549,10 +549,10 @@ zipccl_status zipccl_moe_status(void *stream);
  *   h_k    = act(gate x) * (up x), where gate and up are the first and the last
  *     `inner` rows of expert k's matrix in d_up; ungated: act(up x)
  *   y      = d_residual + sum over the token's experts of weight_k * down_k h_k
- * Sums and h are held in 32 bits; a 32-bit operand takes part with 21 bits at
- * least (two parts of 11), a 16- or 8-bit one exactly.  A token without experts
- * gets its residual, or 0.  A result that something infinite or NaN takes part in
- * is infinite or NaN.
+ * Sums are held in 32 bits.  A 16- or 8-bit operand takes part exactly, a 32-bit
+ * one with 21 bits at least; h takes part with 16 bits where `type` has 16, with
+ * 21 in a 32-bit layer.  A token without experts gets its residual, or 0.  A
+ * result that something infinite or NaN takes part in is infinite or NaN.
  *   d_x [tokens][hidden] of `type`, rows x_stride values apart; d_router
  *     [experts][hidden] of router_type: `type` or F32; d_up [experts]
  *     [gated ? 2 inner : inner][hidden], d_down [experts][hidden][inner]: of

@@ -14,7 +14,8 @@ kernels; there is no CPU path.  PyTorch provides device memory and streams.
 Low-level names mirror the C ABI (``zipccl_compress`` ...) and take raw
 pointers; ``compress`` / ``decompress`` / ``decompress_reduce`` are the same
 calls on torch tensors.  ``operators`` adds what makes and uses the exchanged
-tensors: routing to experts, dispatch and combine, the AdamW step.
+tensors: routing to experts, dispatch and combine, the experts' products, the
+AdamW step.
 """
 from __future__ import annotations
 

@@ -1,6 +1,7 @@
 """Operators around the compressed exchange, on torch tensors: routing to
-experts, the chunk plan, dispatch and combine with their gradients, and the
-AdamW step over many tensors.
+experts, the chunk plan, dispatch and combine with their gradients, the experts'
+products in 8 bits with theirs, the layer for a few tokens, and the AdamW step
+over many tensors.
 
 They make and use what ``compress`` packs: a router's choice and ``moe_plan``
 give the per-expert chunks (``plan.counts * hidden`` is ``chunk_elems``),

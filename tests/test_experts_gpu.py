@@ -543,6 +543,23 @@ def test_layer_agrees_with_the_calls_for_many_tokens():
     assert ((z - x).double() - part).norm() < 3 * 2.0 ** -4 * part.norm()
 
 
+def test_example_runs_in_8_bits_and_its_gradients_are_near_those_of_16():
+    """The example's step with its products in 8 bits: gradients off by the rounding of both operands, 2^-4 of each at
+    most, so by less than 2 * 2^-4 of their norm."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_training_step.py")
+    spec = importlib.util.spec_from_file_location("moe_training_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    torch.manual_seed(10)
+    x, target = torch.randn(500, 192, device="cuda").bfloat16(), torch.randn(500, 192, device="cuda")
+    grads = [example.Layer(192, 5, 8, fp8=fp8).forward_backward(x, target, 2)[1].double() for fp8 in (False, True)]
+    assert (grads[0] - grads[1]).norm() < 2 * 2.0 ** -4 * grads[0].norm()
+    losses, ratio = example.train(steps=2, ranks=2, tokens=300, hidden=200, experts=4, fp8=True)
+    assert all(np.isfinite(losses)) and ratio < 1
+
+
 def test_pointer_level_calls_match_the_tensor_level():
     torch.manual_seed(9)
     s = torch.cuda.current_stream().cuda_stream
