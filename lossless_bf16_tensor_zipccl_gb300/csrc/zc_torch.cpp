@@ -89,7 +89,7 @@ void two_dims(const Tensor& t, const char* what) {
 // Values between the rows of a [tokens, values] CUDA tensor whose rows are contiguous.
 uint64_t row_stride(const Tensor& t, const char* what) {
   two_dims(t, what);
-  if (!t.is_cuda() || (t.stride(1) != 1 && t.size(1) > 1))
+  if (!t.is_cuda() || (t.stride(1) != 1 && t.size(1) > 1 && t.numel() > 0))
     refuse(PyExc_ValueError, "%s: expected a CUDA tensor with contiguous rows", what);
   return (uint64_t)(t.size(0) > 1 ? t.stride(0) : std::max(t.stride(0), t.size(1)));
 }

@@ -8,7 +8,7 @@ Tolerances.
    term is exact.  An instruction adds 32 terms to a 32-bit sum and cuts what is
    below its last places: 2 units of 2^-23 of the magnitudes in play at most, which
    the sum of all magnitudes S bounds.  (terms / 32 + 1) 2^-22 S, and the result's
-   own rounding: half a step, 2^-9 of a bfloat16 value, 2^-12 of a float16 one
+   own rounding: half a step, 2^-8 of a bfloat16 value, 2^-11 of a float16 one
    (2^-25 where that is subnormal), 2^-24 of a float.
  - Layer: each of its three sums, of n terms, is off by (n / 32 + 10) 2^-22 of its
    magnitudes by the same count (chunks are added in ordinary floats, 2^-24 each);
@@ -134,6 +134,7 @@ def test_no_rows_and_given_results():
     for shape in ((0, 256), (4, 0)):
         q = zc.moe_quantize(torch.zeros(shape, device="cuda"))
         assert q.codes.shape == shape
+        assert zc.moe_quantize(torch.zeros(shape, device="cuda").as_strided(shape, (0, 0))).codes.shape == shape
     at = torch.zeros(4, dtype=torch.int32, device="cuda")
     q = zc.moe_quantize_columns(torch.zeros(0, 64, device="cuda"), at)
     assert not bits(q.scales).any() and q.scales.shape == (3, 64)
@@ -210,6 +211,35 @@ def test_products_and_gradients(case):
         near(host(zc.moe_matmul_backward(gr, wq, at, dtype=dtype)), backward[0], tolerance(outer, backward[1], backward[0], dtype))
         near(host(zc.moe_matmul_backward_weights(gc, xc, at, dtype=dtype)), by_weights[0],
              tolerance(most, by_weights[1], by_weights[0], dtype))
+
+
+def test_products_of_a_thousand_chunks():
+    """As many experts as a call takes, most of them without rows."""
+    torch.manual_seed(11)
+    counts = torch.zeros(1024, dtype=torch.int32)
+    counts[[0, 5, 6, 500, 1023]] = torch.tensor([40, 1, 130, 300, 29], dtype=torch.int32)
+    at = torch.cat([torch.zeros(1, dtype=torch.int32), counts.cumsum(0).int()]).cuda()
+    rows = int(counts.sum())
+    x, w = torch.randint(-7, 8, (rows, 128), device="cuda").float(), torch.randint(-7, 8, (1024, 32, 128), device="cuda").float()
+    x[:, 0], w[:, 0, 0] = 7, 7
+    y = zc.moe_matmul(zc.moe_quantize(x), zc.moe_quantize_weights(w), at, dtype=torch.float32)
+    expert = torch.arange(1024).repeat_interleave(counts.long()).cuda()
+    assert torch.equal(y, torch.einsum("mk,mnk->mn", x.double(), w[expert].double()).float())
+    g = torch.randint(-7, 8, (rows, 32), device="cuda").float()
+    gw = zc.moe_matmul_backward_weights(zc.moe_quantize_columns(g, at), zc.moe_quantize_columns(x, at), at, dtype=torch.float32)
+    want = torch.zeros(1024, 32, 128, dtype=torch.float64, device="cuda").index_add_(0, expert, torch.einsum("mn,mk->mnk", g.double(), x.double()))
+    assert torch.equal(gw, want.float())              # whole numbers up to 7 are exact in every block's scale
+    assert not gw[1:5].any() and not gw[7:500].any()
+
+
+def test_layer_of_the_most_tokens_pairs_and_experts():
+    """32 tokens of 32 pairs each, all of 1,024 experts or all of 32: entries of 8 tokens, of 1, and of none."""
+    rng = np.random.default_rng(12)
+    for E in (1024, 32):
+        case = (32, 64, 24, E, 32, True, "silu")
+        x, router, up, down, residual = layer_case(rng, case, torch.float32)
+        got = zc.moe_layer(x, router, up, down, 32, residual=residual)
+        layer_near(got, case, torch.float32, ex.layer(*map(host, (x, router, up, down)), 32, "silu", host(residual)))
 
 
 def test_products_of_whole_numbers_are_exact():
