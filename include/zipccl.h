@@ -563,7 +563,8 @@ zipccl_status zipccl_moe_status(void *stream);
  *     d_weights, d_ids [tokens][top_k], written.
  * act: SILU v / (1 + exp(-v)); GELU v (1 + erf(v / sqrt 2)) / 2; RELU max(v, 0).
  * d_ws: 256-byte aligned, zipccl_moe_layer_workspace_bytes bytes; nothing in it
- * has to be set, and nothing is kept in it.
+ * has to be set, and nothing is kept in it.  Calls that may run at the same time
+ * (on two streams, in two graphs) need workspaces of their own.
  */
 #define ZIPCCL_LAYER_MAX_TOKENS 32u
 typedef enum { ZIPCCL_ACTIVATION_SILU = 0, ZIPCCL_ACTIVATION_GELU = 1, ZIPCCL_ACTIVATION_RELU = 2 } zipccl_activation;

@@ -9,11 +9,10 @@
 // A tile of the result is 256 lanes x up to 256 columns, made by the tensor cores of
 // a pair of multiprocessors together: each has 128 of the lanes and loads half of
 // the columns' operand, so that a multiprocessor takes 64 bytes from the L2 cache
-// for the work of a cycle (alone it would take 96).  The
-// lanes are the matrices' rows (outer or inner places), the columns the chunk's
-// rows: a chunk may have any number of rows, and the columns of an instruction may
-// be any multiple of 32, so that a chunk's end costs at most 31 columns, where the
-// lanes are always full.  In the gradient of the weights lanes are the inner
+// for the work of a cycle (alone it would take 96).  The lanes are the matrices'
+// rows (outer or inner places), the columns the chunk's rows: a chunk may have any
+// number of rows, and the columns of an instruction may be any multiple of 32, so
+// that a chunk's end costs at most 31 columns, where the lanes are always full.  In the gradient of the weights lanes are the inner
 // places, columns the outer ones, and the chunk's rows are summed over.
 // The result thus lies with its contiguous index along the lanes.
 //
@@ -23,6 +22,12 @@
 //
 // The weights are read along the sum forward and across it backward, from the
 // same codes: blocks of 128 x 128 serve both.
+//
+// Measured: 8,192 rows with one matrix of 14,336 x 4,096, 322 us forward and by
+// the rows, 349 by the weights: 2,750 to 2,990 TFLOP/s, where instructions alone run at
+// 4,780.  32,768 rows in 64 chunks with matrices of 2,048 x 4,096: 227, 243 and 361;
+// the last writes 1.07 GB, which at the rate of writes alone (4,050 GB/s) takes 265.
+// Few rows (122 with the same 64): 87 us, 6,100 GB/s of the weights' bytes.
 //
 // Warps: 0 loads tiles through tensor maps, six stages of 128 places ahead; 1 (of
 // the leading block) issues the products; 2 lays the scales out (128 rows x 4
