@@ -550,8 +550,7 @@ zipccl_status zipccl_moe_status(void *stream);
  *     `inner` rows of expert k's matrix in d_up; ungated: act(up x)
  *   y      = d_residual + sum over the token's experts of weight_k * down_k h_k
  * Sums are held in 32 bits.  A 16- or 8-bit operand takes part exactly, a 32-bit
- * one with 21 bits at least; h takes part with 16 bits where `type` has 16, with
- * 21 in a 32-bit layer.  A token without experts gets its residual, or 0.  A
+ * one and h with 21 bits at least.  A token without experts gets its residual, or 0.  A
  * result that something infinite or NaN takes part in is infinite or NaN.
  *   d_x [tokens][hidden] of `type`, rows x_stride values apart; d_router
  *     [experts][hidden] of router_type: `type` or F32; d_up [experts]

@@ -188,27 +188,36 @@ constexpr uint32_t kPlacesOfChunk = kChunk / sizeof(W);
 template <class W>
 constexpr uint32_t kPlacesOfPiece = kPiece / sizeof(W);
 
-// h as the second kernel takes it, each part in an array of its own.  Where the
-// layer's type has 16 bits two bfloat16 values: 16 bits, 2^-17 of h off at most,
-// where the result's own rounding is 2^-8 or 2^-11; half the loads of two floats and
-// two thirds of the products of three.  For 32-bit layers two floats of 11 bits.
-struct TwoSmall {
+// h as the second kernel takes it, each part in an array of its own: with bfloat16
+// weights three bfloat16 values, 24 bits.  With others in a layer of 16 bits the
+// float itself: the instruction drops its low 13 bits, and what they hold is the
+// second part, of which it takes 11 bits (h is 2^-21 off at most, and a part costs
+// no more than to unpack).  For 32-bit layers two floats of 11 bits, made once.
+// (16 bits of h in two bfloat16 values made ten times as many results differ from
+// the rounded sum as 24 do: 0.3% of bfloat16 ones, 0.8% of float16 ones.)
+struct ThreeSmall {
   using Value = __nv_bfloat16;
-  static constexpr int kParts = 2;
+  static constexpr int kParts = 3;
+};
+struct Whole {
+  using Value = float;
+  static constexpr int kParts = 1;
 };
 struct TwoParts {
   using Value = float;
   static constexpr int kParts = 2;
 };
-template <class T>
-using PartsFor = std::conditional_t<sizeof(T) == 2, TwoSmall, TwoParts>;
+template <class T, class W>
+using PartsFor = std::conditional_t<sizeof(T) == 4, TwoParts, std::conditional_t<std::is_same<W, __nv_bfloat16>::value, ThreeSmall, Whole>>;
 template <class X>
 struct PartsOf {  // of a plain vector: itself
   using Value = X;
   static constexpr int kParts = 1;
 };
 template <>
-struct PartsOf<TwoSmall> : TwoSmall {};
+struct PartsOf<ThreeSmall> : ThreeSmall {};
+template <>
+struct PartsOf<Whole> : Whole {};
 template <>
 struct PartsOf<TwoParts> : TwoParts {};
 
@@ -217,17 +226,22 @@ __device__ __forceinline__ float bf16_part(float v) {
   if (isinf(p) && !isinf(v)) p = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
   return p;
 }
-// Writes the parts of v to at[0] and at[apart].
-__device__ __forceinline__ void store_parts(__nv_bfloat16* at, uint64_t apart, float v) {
-  const float p = bf16_part(v);
-  at[0] = __float2bfloat16_rn(p);
-  at[apart] = __float2bfloat16_rn(isfinite(v) ? v - p : 0.0f);
-}
-__device__ __forceinline__ void store_parts(float* at, uint64_t apart, float v) {
-  float hi, lo;
-  parts(v, hi, lo);
-  at[0] = hi;
-  at[apart] = lo;
+// Writes the parts of v to at[0], at[apart], ...
+template <class X>
+__device__ __forceinline__ void store_parts(typename X::Value* at, uint64_t apart, float v) {
+  if constexpr (X::kParts == 1) {
+    at[0] = v;
+  } else if constexpr (X::kParts == 2) {
+    float hi, lo;
+    parts(v, hi, lo);
+    at[0] = hi;
+    at[apart] = lo;
+  } else {
+    const float p = bf16_part(v), r = isfinite(v) ? v - p : 0.0f, q = bf16_part(r);
+    at[0] = __float2bfloat16_rn(p);
+    at[apart] = __float2bfloat16_rn(q);
+    at[2 * apart] = __float2bfloat16_rn(r - q);
+  }
 }
 
 // The part of a vector that belongs to a lane's 16 bytes of weights, as it is read
@@ -286,7 +300,8 @@ __device__ __forceinline__ void step_products(float (&t)[4], const uint4& w0, co
       multiply16<W>(t, w0.z, w1.z, w0.w, w1.w, x.q[i][0].z, x.q[i][0].w);
     }
   } else {
-    constexpr bool kPartsW = std::is_same<W, float>::value, kSplitX = std::is_same<X, float>::value, kSmall = kPartsW || kSplitX || P == 2;
+    constexpr bool kPartsW = std::is_same<W, float>::value, kSplitX = std::is_same<X, float>::value, kWholeX = std::is_same<X, Whole>::value;
+    constexpr bool kSmall = kPartsW || kSplitX || kWholeX || P == 2;
     constexpr int J = kPer16<W> / 2;
 #pragma unroll
     for (int j0 = 0; j0 < J; j0 += 4) {
@@ -304,6 +319,10 @@ __device__ __forceinline__ void step_products(float (&t)[4], const uint4& w0, co
           const float2 u = b;
           parts(u.x, b.x, l.x), parts(u.y, b.y, l.y);
           multiply(small, p.x, q.x, p.y, q.y, l.x, l.y);
+        }
+        if constexpr (kWholeX) {
+          const auto low = [](float v) { return v - __uint_as_float(__float_as_uint(v) & 0xFFFFE000u); };
+          multiply(small, p.x, q.x, p.y, q.y, low(b.x), low(b.y));
         }
         if constexpr (P == 2) {
           const float2 l = x.two(1, j);
@@ -338,7 +357,7 @@ struct Rows {
 template <class W, class X, bool kShift>
 struct Chunk {
   using R = RawShare<W, X, kShift>;
-  static constexpr bool kBothSteps = 2 * sizeof(R) <= 64;
+  static constexpr bool kBothSteps = 2 * sizeof(R) <= (R::S::P == 3 ? 96 : 64);
   R x[kBothSteps ? 2 : 1];
   __device__ __forceinline__ void load(const typename R::Value* p, uint64_t apart, uint32_t k0, uint32_t n) {
     const uint32_t k = k0 + threadIdx.x % 4 * kPer16<W>;

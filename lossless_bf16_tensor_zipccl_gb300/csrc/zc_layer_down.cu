@@ -23,7 +23,7 @@ __host__ __device__ __forceinline__ size_t down_memory(uint32_t tokens, uint32_t
 template <bool kShift, class T, class W>
 __device__ __forceinline__ void layer_down(const LayerArgs& a, const Pairs& pairs, Ring& ring, uint8_t* memory) {
   constexpr uint32_t kRound = kCluster;  // tiles before the blocks' sums are added
-  using X = PartsFor<T>;
+  using X = PartsFor<T, W>;
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, gid = lane / 4, quad = lane % 4;
   const uint32_t rank = cluster_rank(), cluster = blockIdx.x / kCluster, clusters = gridDim.x / kCluster;
   const uint32_t size = a.tokens * 16;  // of a tile: [token][place]
@@ -203,7 +203,7 @@ extern "C" {
 
 zipccl_status zipccl_moe_layer_workspace_bytes(uint64_t tokens, uint32_t top_k, uint64_t inner, uint64_t* out_bytes) {
   if (!out_bytes || tokens > kMaxTokens || top_k == 0 || top_k > kMaxTopK || inner >= (1ull << 22)) return ZIPCCL_ERR_INVALID_ARG;
-  *out_bytes = (tokens * top_k * ((inner + 7) / 8 * 8) * 8 + 255) / 256 * 256;  // two floats a value
+  *out_bytes = (tokens * top_k * ((inner + 7) / 8 * 8) * 8 + 255) / 256 * 256;  // two floats a value at most
   return ZIPCCL_OK;
 }
 

@@ -130,6 +130,7 @@ __device__ __forceinline__ void layer_up(const LayerArgs& a, const Pairs& pairs,
   const Matrix matrix = {&a.up_map, static_cast<const uint8_t*>(a.up), (uint64_t)a.experts * rows, a.up_stride * sizeof(W), a.hidden * (uint32_t)sizeof(W)};
   Stages<kShiftW, Fill> stages(ring, memory, matrix, fill, a.stages, &g_layer_up_ran_out);
   float4* sums = reinterpret_cast<float4*>(memory + a.stages * kStageBytes<kShiftW>);
+  using X = PartsFor<T, W>;
   const uint64_t apart = (uint64_t)a.tokens * a.top_k * a.h_stride;
   const uint32_t k0 = warp * kPlacesOfChunk<W>;
   const auto vector = [&](uint32_t n, uint32_t col) -> const T* {  // of the column of active expert n
@@ -193,12 +194,12 @@ __device__ __forceinline__ void layer_up(const LayerArgs& a, const Pairs& pairs,
       const uint32_t col = quad * 2 + i;
       if (col >= tokens) continue;
       const float w = pairs.weight[begin + col];
-      auto* h = static_cast<typename PartsFor<T>::Value*>(a.h) + (uint64_t)(begin + col) * a.h_stride + i0 + gid;
+      auto* h = static_cast<typename X::Value*>(a.h) + (uint64_t)(begin + col) * a.h_stride + i0 + gid;
       if (a.gated) {
-        if (i0 + gid < a.inner) store_parts(h, apart, w * (activate(a.activation, v4[i]) * v4[2 + i]));
+        if (i0 + gid < a.inner) store_parts<X>(h, apart, w * (activate(a.activation, v4[i]) * v4[2 + i]));
       } else {
-        if (i0 + gid < a.inner) store_parts(h, apart, w * activate(a.activation, v4[i]));
-        if (i0 + gid + 8 < a.inner) store_parts(h + 8, apart, w * activate(a.activation, v4[2 + i]));
+        if (i0 + gid < a.inner) store_parts<X>(h, apart, w * activate(a.activation, v4[i]));
+        if (i0 + gid + 8 < a.inner) store_parts<X>(h + 8, apart, w * activate(a.activation, v4[2 + i]));
       }
     }
   }
