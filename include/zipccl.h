@@ -550,8 +550,10 @@ zipccl_status zipccl_moe_status(void *stream);
  *     `inner` rows of expert k's matrix in d_up; ungated: act(up x)
  *   y      = d_residual + sum over the token's experts of weight_k * down_k h_k
  * Sums are held in 32 bits.  A 16- or 8-bit operand takes part exactly, a 32-bit
- * one and h with 21 bits at least.  A token without experts gets its residual, or 0.  A
- * result that something infinite or NaN takes part in is infinite or NaN.
+ * one and h with 21 bits at least.  A token without experts gets its residual, or 0: a
+ * logit that is NaN or -inf takes no part in the choice, so a token with a NaN has
+ * none.  What something infinite or NaN takes part in, by the experts chosen, is
+ * infinite or NaN.
  *   d_x [tokens][hidden] of `type`, rows x_stride values apart; d_router
  *     [experts][hidden] of router_type: `type` or F32; d_up [experts]
  *     [gated ? 2 inner : inner][hidden], d_down [experts][hidden][inner]: of

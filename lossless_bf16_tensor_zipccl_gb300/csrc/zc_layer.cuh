@@ -288,8 +288,10 @@ struct RawShare {
 // t = 16 rows x 8 vectors over a step: w0 and w1 are 16 bytes of rows gid and
 // gid + 8.  16-bit operands of one type go to m16n8k16 as they are; others become
 // floats.  The instructions cut what they add off: sums of large and small parts
-// are kept apart, and of four instructions at most.
-template <class W, class X>
+// are kept apart, and of four instructions at most.  kLogits: a value that is not
+// finite meets no second part, whose sign or 0 would make infinity a NaN (a token's
+// choice hangs on it; what the experts make of such a value may be either).
+template <class W, class X, bool kLogits = false>
 __device__ __forceinline__ void step_products(float (&t)[4], const uint4& w0, const uint4& w1, const Share<W, X>& x) {
   using Value = typename PartsOf<X>::Value;
   constexpr int P = PartsOf<X>::kParts;
@@ -303,6 +305,7 @@ __device__ __forceinline__ void step_products(float (&t)[4], const uint4& w0, co
     constexpr bool kPartsW = std::is_same<W, float>::value, kSplitX = std::is_same<X, float>::value, kWholeX = std::is_same<X, Whole>::value;
     constexpr bool kSmall = kPartsW || kSplitX || kWholeX || P == 2;
     constexpr int J = kPer16<W> / 2;
+    const auto finite = [](float v) { return kLogits && (__float_as_uint(v) & 0x7FFFFFFFu) >= 0x7F800000u ? 0.0f : v; };
 #pragma unroll
     for (int j0 = 0; j0 < J; j0 += 4) {
       float large[4] = {}, small[4] = {};
@@ -318,7 +321,7 @@ __device__ __forceinline__ void step_products(float (&t)[4], const uint4& w0, co
           float2 l;
           const float2 u = b;
           parts(u.x, b.x, l.x), parts(u.y, b.y, l.y);
-          multiply(small, p.x, q.x, p.y, q.y, l.x, l.y);
+          multiply(small, finite(p.x), finite(q.x), finite(p.y), finite(q.y), l.x, l.y);
         }
         if constexpr (kWholeX) {
           const auto low = [](float v) { return v - __uint_as_float(__float_as_uint(v) & 0xFFFFE000u); };
@@ -328,7 +331,7 @@ __device__ __forceinline__ void step_products(float (&t)[4], const uint4& w0, co
           const float2 l = x.two(1, j);
           multiply(small, p.x, q.x, p.y, q.y, l.x, l.y);
         }
-        if constexpr (kPartsW) multiply(small, pl.x, ql.x, pl.y, ql.y, b.x, b.y);
+        if constexpr (kPartsW) multiply(small, pl.x, ql.x, pl.y, ql.y, finite(b.x), finite(b.y));
         multiply(large, p.x, q.x, p.y, q.y, b.x, b.y);
       }
 #pragma unroll

@@ -64,8 +64,9 @@ __device__ __forceinline__ void router_logits(const LayerArgs& a, float* partial
       for (int u = 0; u < kAhead; ++u) {
         const uint32_t k = (s + u) * kStep<R> + quad * kPer16<R>;
         const int left = s + u < end ? (int)a.hidden - (int)k : 0;
-        step_products<R, T>(t, keep<R>(settle<kShift>(w0[from][u], shift_of(row0)), left), keep<R>(settle<kShift>(w1[from][u], shift_of(row1)), left),
-                            x[from][u].used(v, k, a.hidden, false));
+        // (both zeros behind the warp's share: an infinite value of the next one's would make 0 a NaN)
+        step_products<R, T, true>(t, keep<R>(settle<kShift>(w0[from][u], shift_of(row0)), left),
+                                  keep<R>(settle<kShift>(w1[from][u], shift_of(row1)), left), x[from][u].used(v, k, min(a.hidden, end * kStep<R>), false));
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) c[j] += t[j];

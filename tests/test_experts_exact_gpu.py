@@ -47,3 +47,47 @@ def test_layer_holds_21_bits_of_h(inner, dtype, blocks):
     y, weights, _ = zc.moe_layer(x.to(dtype), torch.ones(1, hidden, dtype=dtype, device="cuda"), *matrices, 1, activation="relu")
     assert (weights == 1).all()
     assert torch.equal(y.double(), ((m[plus] - m[minus]) * 2.0 ** -20).expand(tokens, hidden))
+
+
+@pytest.mark.parametrize("float_router", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("hidden", [64, 256, 1030, 2048, 2050, 7168])
+def test_layer_of_infinite_tokens(hidden, dtype, float_router):
+    """An infinite value makes every logit infinite, by the sign of the router's weight there: experts and weights as
+    moe_route gives for these logits, and nothing of that token's result is finite.  The other tokens do not change."""
+    torch.manual_seed(hidden)
+    experts, inner, tokens = 6, 24, 11
+    router = torch.randn(experts, hidden, device="cuda")
+    router = ((router + router.sign()) * hidden ** -0.5).to(torch.float32 if float_router else dtype)  # none near 0
+    up, down = torch.randn(experts, 2 * inner, hidden, device="cuda").to(dtype), torch.randn(experts, hidden, inner, device="cuda").to(dtype)
+    residual, good = torch.randn(tokens, hidden, device="cuda").to(dtype), torch.randn(tokens, hidden, device="cuda").to(dtype)
+    want = zc.moe_layer(good, router, up, down, 2, residual=residual)
+    for i, at in enumerate(sorted({*range(0, hidden, hidden // 19), 1, hidden // 2 - 1, hidden - 1})):
+        hit = i % tokens
+        x = good.clone()
+        x[hit, at] = float("inf") if i % 2 else float("-inf")
+        logits = x.double() @ router.double().T
+        assert logits[hit].isinf().all()
+        w, ids = zc.moe_route(logits.float(), 2)
+        got = zc.moe_layer(x, router, up, down, 2, residual=residual)
+        assert torch.equal(got[2][hit], ids[hit]) and torch.equal(got[1][hit], w[hit])
+        some = ids[hit, 0] >= 0
+        assert not got[0][hit].isfinite().any() if some else torch.equal(got[0][hit], residual[hit])
+        rest = torch.arange(tokens, device="cuda") != hit
+        assert all(torch.equal(a[rest], b[rest]) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_layer_of_a_token_that_is_not_a_number_and_of_an_infinite_router(dtype):
+    torch.manual_seed(4)
+    router = torch.randn(6, 300, device="cuda").to(dtype)
+    up, down = torch.randn(6, 40, 300, device="cuda").to(dtype), torch.randn(6, 300, 20, device="cuda").to(dtype)
+    x, residual = (torch.randn(3, 300, device="cuda").to(dtype) for _ in range(2))
+    x[1, 77] = float("nan")
+    y, w, ids = zc.moe_layer(x, router, up, down, 2, residual=residual)
+    assert (ids[1] == -1).all() and not w[1].any() and torch.equal(y[1], residual[1]) and y.isfinite().all()
+    x[1, 77] = 1
+    router[3, 200], router[4, 211] = float("inf"), float("-inf")
+    y, w, ids = zc.moe_layer(x, router, up, down, 2)
+    want = zc.moe_route((x.double() @ router.double().T).float(), 2)
+    assert torch.equal(ids, want[1]) and y.isfinite().all()
