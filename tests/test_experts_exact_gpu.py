@@ -91,3 +91,26 @@ def test_layer_of_a_token_that_is_not_a_number_and_of_an_infinite_router(dtype):
     y, w, ids = zc.moe_layer(x, router, up, down, 2)
     want = zc.moe_route((x.double() @ router.double().T).float(), 2)
     assert torch.equal(ids, want[1]) and y.isfinite().all()
+
+
+def _through(gates, factors, activation):
+    """act(gate) * factor for each pair, through a gated layer of one expert: a token's only value is 1, `down` is the unit matrix."""
+    n = gates.numel()
+    x = torch.zeros(1, n, device="cuda")
+    x[0, 0] = 1
+    up = torch.zeros(1, 2 * n, n, device="cuda")
+    up[0, :n, 0], up[0, n:, 0] = gates, factors
+    y, _, _ = zc.moe_layer(x, torch.ones(1, n, device="cuda"), up, torch.eye(n, device="cuda")[None].contiguous(), 1, activation=activation)
+    return y[0].double()
+
+
+def test_gelu_of_negative_gates_is_relatively_near():
+    """erfc's argument is off by 2^-23 of itself at most (the gate's second part 2^-22, the constant and the product
+    2^-24 each): e^(-v^2/2) by v^2 of that.  erfc itself is off by 4 units (CUDA's bound), the products, h and the
+    factor by 2^-21 together."""
+    gates = torch.cat([-torch.linspace(0.01, 12, 500), torch.linspace(0.01, 12, 100)]).cuda()
+    factors = torch.where(torch.arange(600, device="cuda") % 2 > 0, 1e6, 1.0)
+    got = _through(gates, factors, "gelu")
+    v = gates.double()
+    want = 0.5 * v * torch.erfc(-v * 0.5 ** 0.5) * factors.double()
+    assert ((got - want).abs() <= (2.0 ** -20 + v * v * 2.0 ** -21) * want.abs()).all()
