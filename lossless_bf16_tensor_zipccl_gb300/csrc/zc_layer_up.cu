@@ -20,10 +20,11 @@ __device__ __noinline__ Choice choose_any(const RouteArgs& a, const float* row, 
   if (a.experts <= 512) return choose<float, 32, 16>(a, row, live, lane, keys);
   return choose<float, 32, 32>(a, row, live, lane, keys);
 }
-// (GELU by the complement: 1 + erf cancels for v < 0 and is 0 from -5.5 on, where
+// (SiLU: e^-v overflows from v = -88.8 on, where the result is still a normal float;
+// GELU by the complement: 1 + erf cancels for v < 0 and is 0 from -5.5 on, where
 // v (1 + erf) / 2 is still -1e-7.)
 __device__ __forceinline__ float activate(int activation, float v) {
-  if (activation == ZIPCCL_ACTIVATION_SILU) return v / (1.0f + expf(-v));
+  if (activation == ZIPCCL_ACTIVATION_SILU) return v * sigmoid(v);
   if (activation == ZIPCCL_ACTIVATION_GELU) return 0.5f * v * erfcf(v * -0.70710678118654752f);
   return v > 0.0f || isnan(v) ? v : 0.0f;
 }

@@ -114,3 +114,14 @@ def test_gelu_of_negative_gates_is_relatively_near():
     v = gates.double()
     want = 0.5 * v * torch.erfc(-v * 0.5 ** 0.5) * factors.double()
     assert ((got - want).abs() <= (2.0 ** -20 + v * v * 2.0 ** -21) * want.abs()).all()
+
+
+def test_silu_keeps_its_value_down_to_the_smallest_floats():
+    """e^v is off by v times the gate's 2^-22 and 2^-21 of itself, or by a unit of the smallest floats; factor, product
+    and h by 2^-21 together."""
+    gates = torch.linspace(-103, 20, 800, device="cuda")
+    factors = torch.full((800,), 2.0 ** 100, device="cuda")
+    got = _through(gates, factors, "silu")
+    v = gates.double()
+    want = v * v.sigmoid() * factors.double()
+    assert ((got - want).abs() <= (2.0 ** -20 + v.abs() * 2.0 ** -22) * want.abs() + v.abs() * 2.0 ** (100 - 149)).all()
