@@ -394,16 +394,18 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
       // (so that the barrier of its stage is at that turn), this warp of the leading
       // block sees it arrive and tells the other's; both clear their half, before the
       // products come to it.
-      uint32_t n = 0, parity = 0;  // parity: a bit for each stage
+      uint32_t n = 0, before = 0, parity = 0;  // before: blocks up to the last wait; parity: a bit for each stage
       for (uint32_t t = pair; t < total && ok; t += pairs) {
         const Tile x = tile_of<kWeights>(a, s, t, rank);
         n += x.blocks;
         if (x.count % 32 == 0) continue;
         const uint32_t st = (n - 1) % kStages, from = x.count % kPlaces, upto = (from + 31) / 32 * 32;
+        const uint64_t limit = limit_for(n - before);
+        before = n;
         if (rank == 0) {
-          if (!(ok = wait_phase(&s.ends[st], parity >> st & 1)) || !(ok = wait_cluster(&s.full[st], (n - 1) / kStages & 1))) break;
+          if (!(ok = wait_cluster(&s.ends[st], parity >> st & 1, limit)) || !(ok = wait_cluster(&s.full[st], (n - 1) / kStages & 1))) break;
           if (lane == 0) arrive_at(at_rank(&s.clear[st], 1));
-        } else if (!(ok = wait_cluster(&s.clear[st], parity >> st & 1))) {
+        } else if (!(ok = wait_cluster(&s.clear[st], parity >> st & 1, limit))) {
           break;
         }
         parity ^= 1u << st;
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
       if constexpr (kWeights) out += x.chunk * a.out_matrix + x.column0 * a.out_stride;
       else out += x.row * a.out_stride;
       if (x.blocks) {
-        if (!(ok = wait_cluster(&s.done[buffer], (tiles >> 1) & 1))) break;
+        if (!(ok = wait_cluster(&s.done[buffer], (tiles >> 1) & 1, limit_for(x.blocks)))) break;
         tmem_fence_after();
       }
       const uint32_t parts = x.width / 32;

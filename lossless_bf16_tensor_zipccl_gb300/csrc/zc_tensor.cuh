@@ -65,8 +65,8 @@ __device__ __forceinline__ void arrive_at(uint32_t bar) {
 __device__ __forceinline__ void arrive_at_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// As wait_phase, for what blocks of the cluster have arrived on.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
+// As wait_phase, for what blocks of the cluster have arrived on; false after `limit`.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit = kWaitLimitNs) {
   uint64_t t0 = 0;
   while (true) {
     uint32_t done;
@@ -78,9 +78,12 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
     if (done) return true;
     const uint64_t now = globaltimer_ns();
     if (t0 == 0) t0 = now;
-    else if (now - t0 > kWaitLimitNs) return false;
+    else if (now - t0 > limit) return false;
   }
 }
+// The limit of a wait for `blocks` blocks of a sum: 4 us more for each, ten times what
+// one takes at most (one chunk of 900 M rows is 7 M blocks: 2.9 s).
+__device__ __forceinline__ uint64_t limit_for(uint32_t blocks) { return kWaitLimitNs + blocks * 4096ull; }
 
 // ---- tensor maps
 __device__ __forceinline__ void tma_prefetch(const void* map) {

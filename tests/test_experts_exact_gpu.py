@@ -125,3 +125,19 @@ def test_silu_keeps_its_value_down_to_the_smallest_floats():
     v = gates.double()
     want = v * v.sigmoid() * factors.double()
     assert ((got - want).abs() <= (2.0 ** -20 + v.abs() * 2.0 ** -22) * want.abs() + v.abs() * 2.0 ** (100 - 149)).all()
+
+
+def test_gradient_of_the_weights_of_a_chunk_that_takes_longer_than_a_wait():
+    """One chunk of 900 million rows, whose only tile takes longer than the 2 s that a wait has: whole
+    numbers in a few rows, the first and the last among them, zeros in the others."""
+    rows, cols = 900_000_013, 16
+    codes = torch.zeros(rows, cols, dtype=torch.uint8, device="cuda")
+    scales = torch.full((rows // 128 + 1, cols), 127, dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu)
+    at = torch.cat([torch.tensor([0, 127, 128, rows - 14, rows - 13, rows - 1], device="cuda"), torch.randperm(rows // 1000, device="cuda")[:300] * 997])
+    at = at.unique()
+    some = torch.randint(-7, 8, (at.numel(), cols), device="cuda").float()
+    codes[at] = some.to(torch.float8_e4m3fn).view(torch.uint8)
+    blocks = zc.Fp8Blocks(codes.view(torch.float8_e4m3fn), scales)
+    got = zc.moe_matmul_backward_weights(blocks, blocks, dtype=torch.float32)
+    zc.moe_status()
+    assert torch.equal(got, some.T @ some)
