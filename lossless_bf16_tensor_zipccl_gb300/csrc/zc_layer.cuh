@@ -483,8 +483,8 @@ struct Stages {
     __syncwarp();
     if (threadIdx.x % 32 == 0) mbar_arrive(&ring.empty[stage]);
     if (fill.more()) {
-      if (number % kWarps == warp && ok) {
-        ok = wait_phase(&ring.empty[stage], parity);
+      if (number % kWarps == warp) {  // one answer for the warp: ask() names all its lanes
+        ok = __all_sync(kAll, ok && wait_phase(&ring.empty[stage], parity));
         if (ok) ask(stage);
         __syncwarp();
       }

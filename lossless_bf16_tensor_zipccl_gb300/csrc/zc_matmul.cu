@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
       }
       if (t < total) read_scales<kWeights>(a, s, x, k0, later);
       const uint32_t set = sets % kScaleSets;
-      if (!(ok = wait_cluster(&s.scales_empty[set], (sets / kScaleSets & 1) ^ 1))) break;
+      if (!(ok = warp_wait(&s.scales_empty[set], (sets / kScaleSets & 1) ^ 1))) break;
       uint4* to = reinterpret_cast<uint4*>(s.scales[set]) + lane;
 #pragma unroll
       for (int j = 0; j < 3; ++j) to[32 * j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
@@ -403,9 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
         const uint64_t limit = limit_for(n - before);
         before = n;
         if (rank == 0) {
-          if (!(ok = wait_cluster(&s.ends[st], parity >> st & 1, limit)) || !(ok = wait_cluster(&s.full[st], (n - 1) / kStages & 1))) break;
+          if (!(ok = warp_wait(&s.ends[st], parity >> st & 1, limit)) || !(ok = warp_wait(&s.full[st], (n - 1) / kStages & 1))) break;
           if (lane == 0) arrive_at(at_rank(&s.clear[st], 1));
-        } else if (!(ok = wait_cluster(&s.clear[st], parity >> st & 1, limit))) {
+        } else if (!(ok = warp_wait(&s.clear[st], parity >> st & 1, limit))) {
           break;
         }
         parity ^= 1u << st;
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
       if constexpr (kWeights) out += x.chunk * a.out_matrix + x.column0 * a.out_stride;
       else out += x.row * a.out_stride;
       if (x.blocks) {
-        if (!(ok = wait_cluster(&s.done[buffer], (tiles >> 1) & 1, limit_for(x.blocks)))) break;
+        if (!(ok = warp_wait(&s.done[buffer], (tiles >> 1) & 1, limit_for(x.blocks)))) break;
         tmem_fence_after();
       }
       const uint32_t parts = x.width / 32;

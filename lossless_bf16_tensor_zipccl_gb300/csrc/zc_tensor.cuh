@@ -81,6 +81,11 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uin
     else if (now - t0 > limit) return false;
   }
 }
+// The same for a whole warp, with one answer for its lanes: what follows a wait that
+// has run out for some of them only would name lanes that do not come.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit = kWaitLimitNs) {
+  return __all_sync(kAll, wait_cluster(bar, parity, limit));
+}
 // The limit of a wait for `blocks` blocks of a sum: 4 us more for each, ten times what
 // one takes at most (one chunk of 900 M rows is 7 M blocks: 2.9 s).
 __device__ __forceinline__ uint64_t limit_for(uint32_t blocks) { return kWaitLimitNs + blocks * 4096ull; }
