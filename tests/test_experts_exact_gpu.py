@@ -3,12 +3,16 @@ units of 32 bits: what a tolerance by the magnitudes of all terms would let pass
 """
 from __future__ import annotations
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
+import experts_norms as norms  # noqa: E402
 import lossless_bf16_tensor_zipccl_gb300 as zc  # noqa: E402
+from experts_norms import ex  # noqa: E402
+from test_experts_gpu import LAYERS  # noqa: E402
 
 TYPES = [torch.float32, torch.bfloat16, torch.float16]
 
@@ -141,3 +145,51 @@ def test_gradient_of_the_weights_of_a_chunk_that_takes_longer_than_a_wait():
     got = zc.moe_matmul_backward_weights(blocks, blocks, dtype=torch.float32)
     zc.moe_status()
     assert torch.equal(got, some.T @ some)
+
+
+@pytest.mark.parametrize("float_router", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("case", LAYERS, ids=lambda c: "-".join(map(str, c[:5])) + f"-{c[6]}")
+def test_layer_is_near_in_the_norm(case, dtype, float_router):
+    """Plain weights and 8-bit ones, with and without a residual (see experts_norms for the bound)."""
+    rng = np.random.default_rng(sum(case[:5]) + 1)
+    x, router, up, down, residual = norms.draw(rng, case, dtype, torch.float32 if float_router else None)
+    k, act = case[4], case[6]
+    blocks = [zc.moe_quantize_weights(w.cuda()) for w in (up, down)]
+    in_blocks = [ex.weights_values(*ex.quantize_weights(norms.values(w))) for w in (up, down)]
+    for matrices, wv in (([up.cuda(), down.cuda()], [norms.values(w) for w in (up, down)]), (blocks, in_blocks)):
+        for r in (residual, None):
+            got = zc.moe_layer(x.cuda(), router.cuda(), *matrices, k, activation=act, residual=None if r is None else r.cuda())
+            rv = None if r is None else norms.values(r)
+            y, w, ids, _, _ = ex.layer(norms.values(x), norms.values(router), *wv, k, act, rv)
+            assert np.array_equal(got[2].cpu().numpy(), ids)
+            assert norms.weights_off(norms.values(got[1]), w) < 1
+            assert norms.off(norms.values(got[0]), y, rv, dtype) < 1
+
+
+@pytest.mark.parametrize("part", ["x", "up", "down"])
+def test_a_32_bit_layer_takes_second_parts(part):
+    """Values 1 + m 2^-20 whose ones cancel in the sum: what is left is exact, and 0 where an operand has 11 bits."""
+    n = 130
+    m = torch.arange(n, device="cuda").double() % 16
+    x = torch.zeros(2, n, dtype=torch.float64, device="cuda")
+    up, down = (torch.zeros(1, n, n, dtype=torch.float64, device="cuda") for _ in range(2))
+    i = torch.arange(n, device="cuda")
+    if part == "x":        # h = x[i] - x[16]: m[16] is 0, so none is below 0
+        x[:] = 1 + m * 2.0 ** -20
+        up[0, i, i] += 1
+        up[0, :, 16] -= 1
+        down[0, i, i] = 1
+        want = m * 2.0 ** -20
+    elif part == "up":     # (1 + m 2^-20) x[0] - x[1]
+        x[:, :2] = 1
+        up[0, :, 0], up[0, :, 1] = 1 + m * 2.0 ** -20, -1
+        down[0, i, i] = 1
+        want = m * 2.0 ** -20
+    else:                  # (1 + m 2^-20) h[0] - h[1]
+        x[:, 0] = 1
+        up[0, :2, 0] = 1
+        down[0, :, 0], down[0, :, 1] = 1 + m * 2.0 ** -20, -1
+        want = m * 2.0 ** -20
+    y, _, _ = zc.moe_layer(x.float(), torch.ones(1, n, device="cuda"), up.float(), down.float(), 1, activation="relu")
+    assert torch.equal(y.double(), want.expand(2, n))
