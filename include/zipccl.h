@@ -554,12 +554,13 @@ zipccl_status zipccl_moe_status(void *stream);
  * logit that is NaN or -inf takes no part in the choice, so a token with a NaN has
  * none.  What something infinite or NaN takes part in, by the experts chosen, is
  * infinite or NaN.
- *   d_x [tokens][hidden] of `type`, rows x_stride values apart; d_router
- *     [experts][hidden] of router_type: `type` or F32; d_up [experts]
- *     [gated ? 2 inner : inner][hidden], d_down [experts][hidden][inner]: of
- *     `type` (weight_bits those of the type), or 8-bit blocks (weight_bits 8,
- *     scales as zipccl_moe_quantize_weights leaves them); rows up_stride and
- *     down_stride values apart;
+ *   d_x [tokens][hidden] of `type`, rows x_stride values apart (0: all the same,
+ *     else hidden at least);
+ *     d_router [experts][hidden] of router_type: `type` or F32;
+ *     d_up [experts][gated ? 2 inner : inner][hidden], d_down [experts][hidden]
+ *     [inner]: of `type` (weight_bits those of the type), or 8-bit blocks
+ *     (weight_bits 8, scales as zipccl_moe_quantize_weights leaves them); rows
+ *     up_stride and down_stride values apart;
  *     d_residual, d_y [tokens][hidden], d_residual may be d_y;
  *     d_weights, d_ids [tokens][top_k], written.
  * act: SILU v / (1 + exp(-v)); GELU v (1 + erf(v / sqrt 2)) / 2; RELU max(v, 0).

@@ -215,7 +215,7 @@ zipccl_status zipccl_moe_layer(const zipccl_moe_layer_args* l, const zipccl_rout
   if (l->router_type != l->type && l->router_type != ZIPCCL_TYPE_F32) return ZIPCCL_ERR_INVALID_ARG;
   const uint32_t experts = l->experts;
   if (experts == 0 || experts > kMaxExperts || l->tokens > kMaxTokens || l->hidden == 0 || l->inner == 0 || l->hidden >= (1ull << 22) ||
-      l->inner >= (1ull << 22) || (l->x_stride < l->hidden && l->tokens > 1))
+      l->inner >= (1ull << 22) || (l->x_stride < l->hidden && l->x_stride != 0 && l->tokens > 1))
     return ZIPCCL_ERR_INVALID_ARG;
   if (o->top_k == 0 || o->top_k > kMaxTopK || o->top_k > experts) return ZIPCCL_ERR_INVALID_ARG;
   if (o->score != ZIPCCL_SCORE_SOFTMAX && o->score != ZIPCCL_SCORE_SIGMOID) return ZIPCCL_ERR_INVALID_ARG;

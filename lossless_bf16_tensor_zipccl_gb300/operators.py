@@ -218,8 +218,8 @@ def moe_layer(x, router, up, down, top_k: int, *, score: str = "softmax", bias=N
     type or float32; ``up`` [experts, inner or 2 * inner, hidden] (twice as many
     rows: the first half is the gate's) and ``down`` [experts, hidden, inner], both
     of x's type or both ``Fp8Blocks`` from ``moe_quantize_weights``;
-    ``activation`` "silu", "gelu" or "relu".  x may have any row stride.  For more
-    tokens: route, plan, dispatch, ``moe_matmul``, combine."""
+    ``activation`` "silu", "gelu" or "relu".  x may have any row stride, 0
+    (expanded) included.  For more tokens: route, plan, dispatch, ``moe_matmul``, combine."""
     return _done(_native.layer(x, router, up, down, top_k, _choice(_SCORES, "score", score), renormalize, scale, groups,
                                groups_kept, _choice(_GROUP_SCORES, "group_score", group_score), bias, mask,
                                _choice(_ACTIVATIONS, "activation", activation), residual, out, weights, ids, ws,

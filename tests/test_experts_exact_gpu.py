@@ -193,3 +193,14 @@ def test_a_32_bit_layer_takes_second_parts(part):
         want = m * 2.0 ** -20
     y, _, _ = zc.moe_layer(x.float(), torch.ones(1, n, device="cuda"), up.float(), down.float(), 1, activation="relu")
     assert torch.equal(y.double(), want.expand(2, n))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_layer_of_one_row_for_all_tokens(dtype):
+    torch.manual_seed(5)
+    router, up, down = (torch.randn(s, device="cuda").to(dtype) for s in ((6, 200), (6, 80, 200), (6, 200, 40)))
+    mask = torch.tensor([True] * 5 + [False] + [True] * 5, device="cuda")
+    x = torch.randn(1, 200, device="cuda").to(dtype).expand(11, 200)
+    assert x.stride(0) == 0
+    want = zc.moe_layer(x.contiguous(), router, up, down, 2, mask=mask)
+    assert all(torch.equal(a, b) for a, b in zip(zc.moe_layer(x, router, up, down, 2, mask=mask), want))
