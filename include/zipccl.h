@@ -520,7 +520,7 @@ zipccl_status zipccl_moe_quantize_weights(const void *d_w, int type, uint32_t ex
  *       chunk's rows; a: gradients [rows][outer] by columns; b: rows
  *       [rows][inner] by columns; out [experts][outer][inner]
  * Rows behind the last chunk are zeros in `out`, as are the gradients of the
- * weights of an empty chunk.  Sums are held in 32 bits on the tensor cores, in a
+ * weights of an empty chunk.  inner and outer are 1 at least.  Sums are held in 32 bits on the tensor cores, in a
  * fixed order; out_type F32, BF16 or F16, rounded once.  out: rows out_stride
  * values apart, the WEIGHTS form's matrices `outer` rows apart.
  * A wait inside a kernel of this call or of zipccl_moe_layer that runs out (2 s;

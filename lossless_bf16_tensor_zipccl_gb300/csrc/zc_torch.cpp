@@ -627,7 +627,12 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Call call(device, a[6]);
   std::vector<int64_t> shape = by_weights ? std::vector<int64_t>{outer, inner} : std::vector<int64_t>{rows, forward ? outer : inner};
   if (by_weights && offsets) shape.insert(shape.begin(), experts);
-  const Tensor out = call.result(a[5], shape, to, "out");
+  Tensor out = call.result(a[5], shape, to, "out");
+  if (inner == 0 || outer == 0) {  // sums of nothing
+    const c10::cuda::CUDAStreamGuard its(c10::cuda::getStreamFromExternal(call.stream, device.index()));
+    if (out.numel()) out.zero_();
+    return answer(ZIPCCL_OK, {out});
+  }
   return answer(zipccl_moe_matmul(form, &xa, &wb, rows, inner, outer, offsets, (uint32_t)experts, out.data_ptr(), type, shape.back(),
                                   call.stream),
                 {out});

@@ -183,7 +183,8 @@ def _matmul(form, a, b, offsets, dtype, out, stream):
 
 def moe_matmul(rows, weights, offsets=None, *, dtype=torch.bfloat16, out=None, stream=None):
     """Every row times its expert's matrix: out[m] = weights[e] @ rows[m] for the
-    rows of chunk e, [n, outer]; rows behind the last chunk become zeros.
+    rows of chunk e, [n, outer]; rows behind the last chunk become zeros, as does
+    everything where the matrices have no columns.
     ``rows`` from ``moe_quantize``, ``weights`` from ``moe_quantize_weights``;
     without ``offsets`` one matrix [outer, inner] for all rows."""
     return _matmul(_FORWARD, rows, weights, offsets, dtype, out, stream)

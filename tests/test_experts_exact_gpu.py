@@ -204,3 +204,26 @@ def test_layer_of_one_row_for_all_tokens(dtype):
     assert x.stride(0) == 0
     want = zc.moe_layer(x.contiguous(), router, up, down, 2, mask=mask)
     assert all(torch.equal(a, b) for a, b in zip(zc.moe_layer(x, router, up, down, 2, mask=mask), want))
+
+
+@pytest.mark.parametrize("side", [False, True])
+@pytest.mark.parametrize("inner,outer", [(0, 40), (40, 0), (0, 0)])
+def test_products_of_no_places_are_zeros(inner, outer, side):
+    """What the quantizing calls give for widths of 0, multiplied: sums of nothing, or nothing."""
+    at = torch.tensor([0, 3, 9], dtype=torch.int32, device="cuda")
+    stream = torch.cuda.Stream() if side else None
+    x, g, w = torch.ones(10, inner, device="cuda"), torch.ones(10, outer, device="cuda"), torch.ones(2, outer, inner, device="cuda")
+    for offsets, matrices in ((at, w), (None, w[0])):
+        (xr, xc), (gr, gc) = (zc.moe_quantize_columns(t, offsets, by_rows=True) for t in (x, g))
+        wq = zc.moe_quantize_weights(matrices)
+        out = torch.full((10, outer), 5.0, device="cuda")
+        if side:
+            stream.wait_stream(torch.cuda.current_stream())
+        y = zc.moe_matmul(xr, wq, offsets, dtype=torch.float32, out=out, stream=stream)
+        gx = zc.moe_matmul_backward(gr, wq, offsets, stream=stream)
+        gw = zc.moe_matmul_backward_weights(gc, xc, offsets, stream=stream)
+        if side:
+            torch.cuda.current_stream().wait_stream(stream)
+        assert y is out or y.data_ptr() == out.data_ptr()
+        assert y.shape == (10, outer) and not y.any() and gx.shape == (10, inner) and not gx.any()
+        assert gw.shape == matrices.shape
