@@ -520,11 +520,16 @@ zipccl_status zipccl_moe_quantize_weights(const void *d_w, int type, uint32_t ex
  *       chunk's rows; a: gradients [rows][outer] by columns; b: rows
  *       [rows][inner] by columns; out [experts][outer][inner]
  * Rows behind the last chunk are zeros in `out`, as are the gradients of the
- * weights of an empty chunk.  inner and outer are 1 at least.  Sums are held in 32 bits on the tensor cores, in a
- * fixed order; out_type F32, BF16 or F16, rounded once.  out: rows out_stride
- * values apart, the WEIGHTS form's matrices `outer` rows apart.
- * A wait inside a kernel of this call or of zipccl_moe_layer that runs out (2 s;
- * not to be expected) leaves its results undefined and sets a word of the current
+ * weights of an empty chunk.  inner and outer are 1 at least.  out: rows
+ * out_stride values apart, the WEIGHTS form's matrices `outer` rows apart; out_type
+ * F32, BF16 or F16, rounded once from 32 bits.
+ * Sums are held in 32 bits on the tensor cores, in a fixed order.  An instruction
+ * adds 32 terms and cuts off what lies below the sum's last place, where float
+ * additions would round: a sum of n terms is off by (n / 32 + 1) 2^-22 of their
+ * magnitudes' sum at most, and one whose terms have one sign comes out small, by n
+ * 2^-29 of itself at most (measured: 1.5e-6 for 4,096 terms, 9.9e-6 for 16,384).
+ * A wait inside a kernel of this call or of zipccl_moe_layer that runs out (2 s
+ * and 4 us for each 128 terms of a sum; not to be expected) leaves its results undefined and sets a word of the current
  * device that zipccl_moe_status reads and clears: ZIPCCL_OK or ZIPCCL_ERR_TIMEOUT
  * (synchronizes `stream`).
  */

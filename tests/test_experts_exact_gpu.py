@@ -227,3 +227,29 @@ def test_products_of_no_places_are_zeros(inner, outer, side):
         assert y is out or y.data_ptr() == out.data_ptr()
         assert y.shape == (10, outer) and not y.any() and gx.shape == (10, inner) and not gx.any()
         assert gw.shape == matrices.shape
+
+
+@pytest.mark.parametrize("terms", [4096, 16384, 131072])
+def test_long_sums_of_one_sign(terms):
+    """Every instruction cuts less than a unit, 2^-23, of a sum that grows evenly from 0: half of terms / 32 units
+    of the whole, terms 2^-29 (and a hundredth, and the last rounding's 2^-23).  Forward and by the weights."""
+    torch.manual_seed(terms)
+    a, b = (torch.rand(terms, 128, device="cuda") for _ in range(2))
+
+    def spread(scales, *dims):  # of each block, for its places
+        s = torch.exp2(scales.view(torch.uint8).double() - 127)
+        for d in dims:
+            s = s.repeat_interleave(128, d)
+        return s
+
+    ac, bc = (zc.moe_quantize_columns(t) for t in (a, b))
+    values = [q.codes.double() * spread(q.scales, 0)[:terms] for q in (ac, bc)]
+    got = [zc.moe_matmul_backward_weights(ac, bc, dtype=torch.float32)]
+    want = [values[0].T @ values[1]]
+    ar, bw = zc.moe_quantize(a.T.contiguous()), zc.moe_quantize_weights(b.T.contiguous())
+    got.append(zc.moe_matmul(ar, bw, dtype=torch.float32))
+    want.append((ar.codes.double() * spread(ar.scales, 1)) @ (bw.codes.double() * spread(bw.scales, 0, 1)).T)
+    for g, w in zip(got, want):
+        off = (w - g.double()) / w
+        assert off.abs().max() <= terms * 2.0 ** -29 * 1.01 + 2.0 ** -23
+        assert off.mean() > 0 or terms < 16384   # cut, not rounded: a sum of one sign comes out small
