@@ -548,7 +548,9 @@ PyObject* quantize_columns(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t experts;
   const int32_t* offsets = chunk_offsets(a[1], x.device(), &experts);
   if (bad_widths(cols) || bad_chunks(experts)) return refused();
-  const bool both = PyObject_IsTrue(a[2]) == 1;
+  const int asked = PyObject_IsTrue(a[2]);
+  if (asked < 0) throw python_error();
+  const bool both = asked == 1;
   if (!both && a[4] != Py_None) refuse(PyExc_ValueError, "rows_out is given and by_rows is not");
   const Call call(x.device(), a[5]);
   const Blocks b = new_blocks(call, a[3], {rows, cols}, {rows / (int64_t)ZIPCCL_FP8_BLOCK + experts, cols}, "out");
