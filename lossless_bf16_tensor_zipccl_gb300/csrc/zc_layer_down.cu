@@ -162,12 +162,6 @@ __global__ void __launch_bounds__(kThreads, 2) zc_layer_down_kernel(const __grid
   pdl_trigger();
 }
 
-// experts that a lane of choose_any holds
-uint32_t held_by_lane(uint32_t experts) {
-  return experts <= 64 ? 2 : experts <= 128 ? 4 : experts <= 256 ? 8 : experts <= 512 ? 16 : 32;
-}
-
-
 template <bool kShift, class T, class W>
 cudaError_t down_launch(LayerArgs a, cudaStream_t s) {
   static std::atomic<int> known[kMaxDevices];
@@ -276,7 +270,7 @@ zipccl_status zipccl_moe_layer(const zipccl_moe_layer_args* l, const zipccl_rout
       (!a.shift_down && !word_map(&a.down_map, l->d_down, l->inner * wz, experts * l->hidden, l->down_stride * wz, kPiece / 8, 8)))
     return ZIPCCL_ERR_CUDA;
   RouteArgs& r = a.route;
-  const uint32_t V = held_by_lane(experts), B = V < 4 ? V : 4;
+  const uint32_t L = lanes_of_token(experts, o->top_k, o->groups), V = experts_of_lane(experts, L), B = V < 4 ? V : 4;
   r.bias = l->d_bias;
   r.mask = l->d_mask;
   r.experts = experts;
@@ -286,7 +280,7 @@ zipccl_status zipccl_moe_layer(const zipccl_moe_layer_args* l, const zipccl_rout
   r.group_size = experts / o->groups;
   r.scale = o->scale;
   const uint32_t lanes = r.group_size % V ? 0 : r.group_size / V;
-  r.group_lanes = lanes & (lanes - 1) || r.groups > 32 ? 0 : lanes;
+  r.group_lanes = lanes & (lanes - 1) || r.groups > L ? 0 : lanes;
   r.softmax = o->score == ZIPCCL_SCORE_SOFTMAX;
   r.renormalize = o->renormalize != 0;
   r.top2 = o->group_score == ZIPCCL_GROUP_TOP2;

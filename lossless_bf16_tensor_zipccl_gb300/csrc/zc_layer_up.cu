@@ -13,12 +13,18 @@ namespace {
 
 __device__ unsigned int g_layer_up_ran_out;
 
+// As the routing call chooses, in the same order.  A warp has one token: where 8 lanes
+// take it, the others have none.
 __device__ __noinline__ Choice choose_any(const RouteArgs& a, const float* row, bool live, uint32_t lane, float* keys) {
-  if (a.experts <= 64) return choose<float, 32, 2>(a, row, live, lane, keys);
-  if (a.experts <= 128) return choose<float, 32, 4>(a, row, live, lane, keys);
-  if (a.experts <= 256) return choose<float, 32, 8>(a, row, live, lane, keys);
-  if (a.experts <= 512) return choose<float, 32, 16>(a, row, live, lane, keys);
-  return choose<float, 32, 32>(a, row, live, lane, keys);
+  const uint32_t lanes = lanes_of_token(a.experts, a.top_k, a.groups);
+  if (lanes == 8) return choose<float, 8, 8>(a, row, live && lane < 8, lane % 8, keys + lane / 8 * 64);
+  switch (experts_of_lane(a.experts, lanes)) {
+    case 2: return choose<float, 32, 2>(a, row, live, lane, keys);
+    case 4: return choose<float, 32, 4>(a, row, live, lane, keys);
+    case 8: return choose<float, 32, 8>(a, row, live, lane, keys);
+    case 16: return choose<float, 32, 16>(a, row, live, lane, keys);
+    default: return choose<float, 32, 32>(a, row, live, lane, keys);
+  }
 }
 // (SiLU: e^-v overflows from v = -88.8 on, where the result is still a normal float;
 // GELU by the complement: 1 + erf cancels for v < 0 and is 0 from -5.5 on, where

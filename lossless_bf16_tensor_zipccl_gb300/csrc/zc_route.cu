@@ -122,19 +122,17 @@ cudaError_t route_launch(RouteArgs a, bool backward, cudaStream_t s) {
   return launch(backward ? zc_route_backward_kernel<T, L, V> : zc_route_kernel<T, L, V>, grid, kRouteThreads, 0, s, a);
 }
 
-// A warp takes a token; 8 lanes do where they hold its experts, 8 each, its
-// pairs and its groups: 16,384 tokens of 64 experts, two chosen, 3.4 us against
-// 5.6 with 32 lanes, one token 2.6 against 2.3.  (Between 65 and 128 experts 16
-// lanes made no difference, nor did they up to 256.)
 template <class T>
 cudaError_t route_by_experts(const RouteArgs& a, bool backward, cudaStream_t s) {
-  const uint32_t e = a.experts;
-  if (e <= 64 && a.top_k <= 8 && a.groups <= 8) return route_launch<T, 8, 8>(a, backward, s);
-  if (e <= 64) return route_launch<T, 32, 2>(a, backward, s);
-  if (e <= 128) return route_launch<T, 32, 4>(a, backward, s);
-  if (e <= 256) return route_launch<T, 32, 8>(a, backward, s);
-  if (e <= 512) return route_launch<T, 32, 16>(a, backward, s);
-  return route_launch<T, 32, 32>(a, backward, s);
+  const uint32_t lanes = lanes_of_token(a.experts, a.top_k, a.groups);
+  if (lanes == 8) return route_launch<T, 8, 8>(a, backward, s);
+  switch (experts_of_lane(a.experts, lanes)) {
+    case 2: return route_launch<T, 32, 2>(a, backward, s);
+    case 4: return route_launch<T, 32, 4>(a, backward, s);
+    case 8: return route_launch<T, 32, 8>(a, backward, s);
+    case 16: return route_launch<T, 32, 16>(a, backward, s);
+    default: return route_launch<T, 32, 32>(a, backward, s);
+  }
 }
 
 zipccl_status route(RouteArgs& a, int type, const zipccl_route_options* o, uint64_t tokens, uint32_t experts,

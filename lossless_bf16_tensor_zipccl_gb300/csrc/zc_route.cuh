@@ -178,6 +178,18 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, float (&c)[V], f
   }
 }
 
+// Lanes that take a token, and experts that a lane holds: the sums over a token go by
+// both, so that every call that chooses asks here.  A warp takes a token; 8 lanes do
+// where they hold its experts, 8 each, its pairs and its groups: 16,384 tokens of 64
+// experts, two chosen, 3.4 us against 5.6 with 32 lanes, one token 2.6 against 2.3.
+// (Between 65 and 128 experts 16 lanes made no difference, nor did they up to 256.)
+__host__ __device__ __forceinline__ uint32_t lanes_of_token(uint32_t experts, uint32_t top_k, uint32_t groups) {
+  return experts <= 64 && top_k <= 8 && groups <= 8 ? 8 : 32;
+}
+__host__ __device__ __forceinline__ uint32_t experts_of_lane(uint32_t experts, uint32_t lanes) {
+  return lanes == 8 ? 8 : experts <= 64 ? 2 : experts <= 128 ? 4 : experts <= 256 ? 8 : experts <= 512 ? 16 : 32;
+}
+
 // A pair of a token: the expert (-1: none) and its weight before the scale.
 struct Choice {
   int32_t id;

@@ -253,3 +253,21 @@ def test_long_sums_of_one_sign(terms):
         off = (w - g.double()) / w
         assert off.abs().max() <= terms * 2.0 ** -29 * 1.01 + 2.0 ** -23
         assert off.mean() > 0 or terms < 16384   # cut, not rounded: a sum of one sign comes out small
+
+
+@pytest.mark.parametrize("experts,groups,k", [(6, 1, 2), (8, 4, 3), (40, 1, 4), (40, 5, 8), (40, 20, 4), (63, 9, 2), (64, 1, 9), (64, 8, 8), (100, 1, 4), (300, 1, 6)])
+def test_layer_has_the_routing_calls_bits(experts, groups, k):
+    """Weights and ids for logits that are whole sixteenths, exact in any order: softmax over all experts, added to a
+    bias or as it is, sums its terms in the order of the routing call."""
+    torch.manual_seed(experts + k)
+    for seed in range(6):
+        x, router = torch.randint(-3, 4, (32, 96), device="cuda").bfloat16(), (torch.randint(-2, 3, (experts, 96), device="cuda") / 16).bfloat16()
+        up, down = torch.zeros(experts, 16, 96, device="cuda").bfloat16(), torch.zeros(experts, 96, 16, device="cuda").bfloat16()
+        bias = torch.randint(-9, 10, (experts,), device="cuda") * 1e-2
+        mask = torch.rand(32, device="cuda") < 0.9
+        for how in (dict(), dict(renormalize=False), dict(score="sigmoid", renormalize=False, scale=2.5), dict(bias=bias),
+                    dict(bias=bias, renormalize=False, mask=mask), dict(bias=bias, score="sigmoid")):
+            how.update(groups=groups, groups_kept=max(1, (groups + 1) // 2), group_score="top2" if seed % 2 else "max")
+            got = zc.moe_layer(x, router, up, down, k, **how)
+            w, ids = zc.moe_route(x.float() @ router.float().T, k, **how)
+            assert torch.equal(got[2], ids) and torch.equal(got[1], w)
