@@ -10,10 +10,11 @@
 // GFLOP.  The tokens are the narrow side: a warp takes 16 rows of a matrix and
 // up to 8 of the expert's tokens to a tensor instruction, which costs no more than one
 // token and less than their sums in ordinary instructions.  16-bit operands of one
-// type go to it as they are (m16n8k16); others as 32-bit floats of which the top 19
-// bits count (m16n8k8): 16-bit and 8-bit values are exact in these, a 32-bit one is
-// the sum of two such parts (21 bits at least), and of products of parts only the
-// two least ones' is left out.
+// type go to it as they are (m16n8k16): x with weights of its type, and h, in parts,
+// with bfloat16 weights; others as 32-bit floats of which the top 19 bits count
+// (m16n8k8): 16-bit and 8-bit values are exact in these, a 32-bit one is the sum of
+// two such parts (21 bits at least), and of products of parts only the two least
+// ones' is left out.
 //
 // Everything that depends on where a place of the sum lies in an instruction is
 // the same for both operands, so a lane reads 16 consecutive bytes of a row and
@@ -29,12 +30,12 @@
 // condition, or the load is waited for at once (142 us instead of 199 for the one
 // token).
 //
-// Measured, both kernels and the choice: that token 131 us, 80% of the copy rate;
-// 32 tokens, 8 of 128 experts of 3 x 2,048 x 768 237 us, 67%; 7 tokens, 2 of 64 of
-// 3 x 4,096 x 2,048: 129 us in 16 bits, 74%, 125 in 8, 38%: there turning codes into
-// floats takes half of the issue slots, and each warp waits for its own; 375 in 32,
+// Measured, both kernels and the choice: that token 134 us, 79% of the copy rate;
+// 32 tokens, 8 of 128 experts of 3 x 2,048 x 768 244 us, 65%; 7 tokens, 2 of 64 of
+// 3 x 4,096 x 2,048: 128 us in 16 bits, 75%, 121 in 8, 40%: there turning codes into
+// floats takes half of the issue slots, and each warp waits for its own; 373 in 32,
 // 51%, for six instructions in place of one.  Rows that start anywhere cost 1.3 to
-// 1.6 times that.
+// 1.7 times that.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -287,10 +288,14 @@ struct RawShare {
 
 // t = 16 rows x 8 vectors over a step: w0 and w1 are 16 bytes of rows gid and
 // gid + 8.  16-bit operands of one type go to m16n8k16 as they are; others become
-// floats.  The instructions cut what they add off: sums of large and small parts
-// are kept apart, and of four instructions at most.  kLogits: a value that is not
-// finite meets no second part, whose sign or 0 would make infinity a NaN (a token's
-// choice hangs on it; what the experts make of such a value may be either).
+// floats.  The instructions cut what lies below a sum's last place: in floats, sums
+// of large and small parts are kept apart, and of four instructions at most; 16-bit
+// operands make one chain of a chunk's instructions, 12 with three parts, the least
+// parts first in each step (2^-20 of the chunk's sum at most, where a result of 16
+// bits has 2^-8 or 2^-11).
+// kLogits: a value that is not finite meets no second part, whose sign or 0 would
+// make infinity a NaN (a token's choice hangs on it; what the experts make of such a
+// value may be either).
 template <class W, class X, bool kLogits = false>
 __device__ __forceinline__ void step_products(float (&t)[4], const uint4& w0, const uint4& w1, const Share<W, X>& x) {
   using Value = typename PartsOf<X>::Value;

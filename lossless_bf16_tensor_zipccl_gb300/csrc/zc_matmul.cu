@@ -12,9 +12,10 @@
 // for the work of a cycle (alone it would take 96).  The lanes are the matrices'
 // rows (outer or inner places), the columns the chunk's rows: a chunk may have any
 // number of rows, and the columns of an instruction may be any multiple of 32, so
-// that a chunk's end costs at most 31 columns, where the lanes are always full.  In the gradient of the weights lanes are the inner
-// places, columns the outer ones, and the chunk's rows are summed over.
-// The result thus lies with its contiguous index along the lanes.
+// that a chunk's end costs at most 31 columns, where the lanes are always full.  In
+// the gradient of the weights lanes are the inner places, columns the outer ones, and
+// the chunk's rows are summed over.  The result thus lies with its contiguous index
+// along the lanes.
 //
 // Two tiles have room in tensor memory beside the scales but for 32 columns: the
 // next tile's first 32 columns are the last 32 of a full one, which are read
@@ -56,7 +57,10 @@ constexpr uint32_t kColumns = 256, kOwnColumns = 128, kPlaces = 128;  // columns
 constexpr uint32_t kStages = 6;
 constexpr uint32_t kBytesA = kOwnLanes * kPlaces, kBytesB = kOwnColumns * kPlaces, kStageBytes = kBytesA + kBytesB;
 constexpr uint32_t kScaleSets = 4, kScaleBytes = 512 * 3;  // four blocks' scales: 128 lanes, 256 columns
-constexpr uint32_t kBoxRows = 16, kBoxes = 4;  // copies of 16, 32, 64 and 128 rows: as many as half a tile's columns need
+// Copies of 16, 32, 64 and 128 rows: as many as half a tile's columns need (with 16 rows
+// alone 8,192 rows with 14,336 x 4,096 take 377 us in place of 323, 32,768 with 64
+// matrices of 2,048 x 4,096 252 in place of 227).
+constexpr uint32_t kBoxRows = 16, kBoxes = 4;
 // Tensor memory: sums from columns 0 and 224 on, scales behind them, 16 columns for each of two sets.
 constexpr uint32_t kSecond = 224, kScaleColumns = kSecond + kColumns;
 
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) zc_matmul_kernel(const __grid_con
           tmem_fence_after();
           const uint32_t at = smem_addr(s.stage[st]);
           for (uint32_t i = 0; i < steps; ++i)
-            product(sums, operand(at + i * (kAcrossA ? 4096 : 32), 0), operand(at + kBytesA + i * (kAcrossB ? 4096 : 32), 0),
+            product(sums, operand(at + i * (kAcrossA ? 4096 : 32)), operand(at + kBytesA + i * (kAcrossB ? 4096 : 32)),
                     with_scale(word, k % 4), scales, scales + 4, k + i > 0);
           tensor_commit(&s.empty[st]);
         }

@@ -173,10 +173,9 @@ __device__ __forceinline__ void store_turned(uint32_t at, uint32_t m0, uint32_t 
 // pieces exchanged as a 128-byte swizzled tensor copy leaves them, 8 lines to
 // the next 1,024 bytes.  Along the sum: a line holds 128 places of the sum (an
 // instruction takes 32, a quarter line further each).  Across it: a line holds
-// one place of the sum for 128 rows of the operand, `apart` bytes to the next
-// 128 rows (an instruction takes 32 lines).
-__device__ __forceinline__ uint64_t operand(uint32_t smem, uint32_t apart) {
-  return (uint64_t)((smem & 0x3FFFFu) >> 4) | (uint64_t)(apart >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// one place of the sum for the operand's 128 rows (an instruction takes 32 lines).
+__device__ __forceinline__ uint64_t operand(uint32_t smem) {
+  return (uint64_t)((smem & 0x3FFFFu) >> 4) | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 // The same for scales: 512 bytes, plain.
 __device__ __forceinline__ uint64_t scale_operand(uint32_t smem) {

@@ -204,8 +204,9 @@ def moe_matmul_backward_weights(grad_columns, columns, offsets=None, *, dtype=to
 
 
 def moe_status(stream=None) -> None:
-    """Raises ``ZipcclError`` if a wait inside a ``moe_matmul`` call on the
-    current device has run out since the last such call (synchronizes)."""
+    """Raises ``ZipcclError`` if a wait inside a ``moe_matmul`` or ``moe_layer``
+    call (or a gradient's) on the current device has run out since ``moe_status``
+    was last called (synchronizes)."""
     handle = torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
     _check(load().zipccl_moe_status(handle), "zipccl_moe_status")
 
